@@ -9,6 +9,7 @@ the C names (``ma_partition``, ``muon_step_batched``, ``adamw_step_fused``,
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Sequence
 
@@ -22,7 +23,8 @@ __all__ = [
     "ma_plan_describe", "ma_plan_destroy", "ma_plan_status", "ma_device_status", "ma_device_status_async",
     "ma_set_wait_limit_ns", "ma_set_momentum_overlap", "ma_debug_build", "MA_ERR_BOUNDS",
     "ma_selftest_wait_timeout", "ma_profile_enable", "ma_profile_collect", "PROF_CLASSES", "group_table", "Plan",
-    "MuonAdamW", "muon_hparams", "adamw_hparams",
+    "MuonAdamW", "muon_hparams", "adamw_hparams", "CLIP_BYTES", "clip_buffer", "ma_grad_norm", "ma_grad_clip",
+    "ma_clip_finalize", "ma_plan_set_clip", "GradClip",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -124,6 +126,16 @@ def lib() -> ctypes.CDLL:
         "muon_step_batched": (i32, [i32, i64, i64, pp, pp, i32, pp, ctypes.POINTER(MuonHParams), vp, sz, vp]),
         "ns_iterate_workspace_bytes": (sz, [i32, i64, i64]),
         "ns_iterate_bf16": (i32, [i32, i64, i64, vp, vp, ctypes.POINTER(ctypes.c_float), i32, i32, vp, sz, vp]),
+        "ma_grad_norm": (i32, [i32, pp, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int64), ctypes.c_float,
+                               ctypes.c_float, vp, vp]),
+        "ma_grad_clip": (i32, [i32, pp, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int64), ctypes.c_float,
+                               ctypes.c_float, vp, vp]),
+        "ma_clip_finalize": (i32, [ctypes.c_float, ctypes.c_float, vp, vp]),
+        "adamw_step_fused_clipped": (i32, [i32, pp, pp, i32, pp, pp, ctypes.POINTER(ctypes.c_int64),
+                                           ctypes.POINTER(AdamWHParams), vp, vp]),
+        "muon_step_batched_clipped": (i32, [i32, i64, i64, pp, pp, i32, pp, ctypes.POINTER(MuonHParams), vp, vp, sz,
+                                            vp]),
+        "ma_plan_set_clip": (i32, [vp, i32, ctypes.c_float, ctypes.c_float, vp]),
         "adamw_step_fused": (i32, [i32, pp, pp, i32, pp, pp, ctypes.POINTER(ctypes.c_int64),
                                    ctypes.POINTER(AdamWHParams), vp]),
         "ma_plan_create": (i32, [ctypes.POINTER(Tensor), i32, ctypes.POINTER(Group), i32, ctypes.POINTER(vp),
@@ -281,8 +293,9 @@ def muon_workspace_bytes(batch: int, R: int, C: int, hp: MuonHParams) -> int:
 
 
 def muon_step_batched(W, G, M, hp: MuonHParams, ws, ws_bytes: int | None = None, stream=None,
-                      gdt: int | None = None, shape=None) -> None:
-    """One Muon step on same-shape matrices. W, G, M: sequences of torch tensors (or device pointers)."""
+                      gdt: int | None = None, shape=None, clip=None) -> None:
+    """One Muon step on same-shape matrices. W, G, M: sequences of torch tensors (or device pointers).
+    clip: a clip buffer whose coefficient multiplies the gradients as they are read (see ma_grad_norm)."""
     batch = len(W)
     if shape is None:
         R, C = (int(W[0].shape[0]), int(W[0].shape[1])) if batch else (0, 0)
@@ -292,8 +305,8 @@ def muon_step_batched(W, G, M, hp: MuonHParams, ws, ws_bytes: int | None = None,
         gdt = _dtype_code(G[0]) if batch else MA_F32
     if ws_bytes is None:
         ws_bytes = ws.numel() * ws.element_size() if ws is not None else 0
-    _check(lib().muon_step_batched(batch, R, C, _ptr_array(W), _ptr_array(G), int(gdt), _ptr_array(M),
-                                   ctypes.byref(hp), _ptr(ws), int(ws_bytes), _stream(stream)),
+    _check(lib().muon_step_batched_clipped(batch, R, C, _ptr_array(W), _ptr_array(G), int(gdt), _ptr_array(M),
+                                           ctypes.byref(hp), _ptr(clip), _ptr(ws), int(ws_bytes), _stream(stream)),
            "muon_step_batched")
 
 
@@ -334,16 +347,75 @@ def ns_iterate_bf16(X_in, X_out, coeffs, steps: int, ws, ws_bytes: int | None = 
                                  int(ws_bytes), _stream(stream)), "ns_iterate_bf16")
 
 
-def adamw_step_fused(P, G, M, V, hp: AdamWHParams, stream=None, gdt: int | None = None, numel=None) -> None:
-    """One multi-tensor AdamW step over parallel lists of fp32 params, gradients, exp_avg and exp_avg_sq."""
+def adamw_step_fused(P, G, M, V, hp: AdamWHParams, stream=None, gdt: int | None = None, numel=None,
+                     clip=None) -> None:
+    """One multi-tensor AdamW step over parallel lists of fp32 params, gradients, exp_avg and exp_avg_sq.
+    clip: a clip buffer whose coefficient multiplies the gradients as they are read (see ma_grad_norm)."""
     n = len(P)
     if gdt is None:
         gdt = _dtype_code(G[0]) if n else MA_F32
     if numel is None:
         numel = [int(p.numel()) for p in P]
     nar = (ctypes.c_int64 * max(1, n))(*numel)
-    _check(lib().adamw_step_fused(n, _ptr_array(P), _ptr_array(G), int(gdt), _ptr_array(M), _ptr_array(V), nar,
-                                  ctypes.byref(hp), _stream(stream)), "adamw_step_fused")
+    _check(lib().adamw_step_fused_clipped(n, _ptr_array(P), _ptr_array(G), int(gdt), _ptr_array(M), _ptr_array(V),
+                                          nar, ctypes.byref(hp), _ptr(clip), _stream(stream)), "adamw_step_fused")
+
+
+CLIP_BYTES = 16640  # MA_CLIP_BYTES
+
+
+def clip_buffer(device=None):
+    """A clip buffer (fp32 tensor of CLIP_BYTES): element 0 is the norm, 1 the coefficient, and elements 2..3 hold
+    the sum of squares as one double. It needs no initial value."""
+    import torch
+    return torch.empty(CLIP_BYTES // 4, dtype=torch.float32, device=device or "cuda")
+
+
+def _on_current_gpu(what: str, *tensors) -> None:
+    """Refuse tensors that are not on the current CUDA device (the one the launch goes to)."""
+    import torch
+    for t in tensors:
+        if t is not None and not (t.is_cuda and t.device.index == torch.cuda.current_device()):
+            raise MAError(MA_ERR_ARG, f"{what}: tensor on {t.device}, not on the current CUDA device")
+
+
+def _grad_tables(G):
+    """Pointer, dtype and element-count arrays of a list of gradients (contiguous tensors)."""
+    n = len(G)
+    for g in G:
+        if not g.is_contiguous():
+            raise MAError(MA_ERR_SHAPE, "gradients must be contiguous")
+    return (n, _ptr_array(G), (ctypes.c_int32 * max(1, n))(*[_dtype_code(g) for g in G]),
+            (ctypes.c_int64 * max(1, n))(*[int(g.numel()) for g in G]))
+
+
+def ma_grad_norm(G, clip, max_norm: float = math.inf, scale: float = 1.0, stream=None) -> None:
+    """Global norm of a list of gradients (fp32 or bf16, any mix) into the clip buffer: norm = scale * sqrt(sum g^2)
+    and coef = scale * min(1, max_norm / norm), 0 when the norm is not finite. The gradients are left alone:
+    adamw_step_fused, muon_step_batched and the plan's steps take them times coef."""
+    _on_current_gpu("ma_grad_norm", clip, *G)
+    _check(lib().ma_grad_norm(*_grad_tables(G), float(scale), float(max_norm), _ptr(clip), _stream(stream)),
+           "ma_grad_norm")
+
+
+def ma_grad_clip(G, clip, max_norm: float, scale: float = 1.0, stream=None) -> None:
+    """ma_grad_norm, then every gradient times coef, in place (zero, whatever it holds, where coef is 0)."""
+    _on_current_gpu("ma_grad_clip", clip, *G)
+    _check(lib().ma_grad_clip(*_grad_tables(G), float(scale), float(max_norm), _ptr(clip), _stream(stream)),
+           "ma_grad_clip")
+
+
+def ma_clip_finalize(clip, max_norm: float = math.inf, scale: float = 1.0, stream=None) -> None:
+    """Norm and coef again from the buffer's sum of squares (after the sums of several ranks were added)."""
+    _on_current_gpu("ma_clip_finalize", clip)
+    _check(lib().ma_clip_finalize(float(scale), float(max_norm), _ptr(clip), _stream(stream)), "ma_clip_finalize")
+
+
+def ma_plan_set_clip(plan, clip, max_norm: float = math.inf, scale: float = 1.0, measure: bool = True) -> None:
+    """Clip the gradients of the plan's later steps by their global norm, through this buffer (None: off again).
+    measure=False: the steps take the coefficient the buffer holds by then, and fill nothing."""
+    _check(lib().ma_plan_set_clip(plan, int(bool(measure)), float(scale), float(max_norm), _ptr(clip)),
+           "ma_plan_set_clip")
 
 
 def ma_plan_create(tensors: Sequence[Tensor], groups: Sequence[Group], ws_cap: int = 0):
@@ -434,7 +506,7 @@ def ma_selftest_wait_timeout(limit_ns: int, stream=None) -> None:
 
 
 PROF_CLASSES = ("adamw", "momentum", "finalize", "ns_gram", "ns_apply", "ns_gramsq", "ns_final", "momentum_side",
-                "ns_q1")
+                "ns_q1", "clip")
 
 
 def ma_profile_enable(on: bool) -> None:
@@ -468,6 +540,36 @@ def group_table(groups) -> list:
     return table
 
 
+class GradClip:
+    """Global norm and clipping of a fixed list of gradients (contiguous fp32 or bf16 tensors on one GPU).
+
+    Keeps the pointer tables, so that a call costs a few microseconds of host
+    time, and the clip ``buffer`` that the steps take. The gradients stay at
+    their addresses (as persistent ``.grad`` tensors do). Calls that overlap on
+    the GPU need an object each.
+    """
+
+    def __init__(self, grads):
+        self.grads = list(grads)
+        _on_current_gpu("GradClip", *self.grads)
+        self._tables = _grad_tables(self.grads)
+        self.buffer = clip_buffer()
+        self._norm = self.buffer[0]
+        self._ptr = _ptr(self.buffer)
+
+    def norm(self, max_norm: float = math.inf, scale: float = 1.0, stream=None):
+        """Fill ``buffer``; the norm (times scale) as a 0-d view of it, on the device. The next call overwrites it."""
+        _on_current_gpu("GradClip.norm", self.buffer)
+        _check(lib().ma_grad_norm(*self._tables, scale, max_norm, self._ptr, _stream(stream)), "ma_grad_norm")
+        return self._norm
+
+    def clip(self, max_norm: float, scale: float = 1.0, stream=None):
+        """Scale and clip the gradients in place; returns their norm before clipping, as :meth:`norm` does."""
+        _on_current_gpu("GradClip.clip", self.buffer)
+        _check(lib().ma_grad_clip(*self._tables, scale, max_norm, self._ptr, _stream(stream)), "ma_grad_clip")
+        return self._norm
+
+
 class Plan:
     """Owns an ma_plan_t and its device workspace (a torch uint8 buffer)."""
 
@@ -486,6 +588,11 @@ class Plan:
                        copy_stream=None) -> None:
         muonadamw_step_from_host(self.handle, groups if groups is not None else self.groups, host_grads, self.ws,
                                  self.ws.numel(), stream, copy_stream)
+
+    def set_clip(self, clip, max_norm: float = math.inf, scale: float = 1.0) -> None:
+        """Clip the gradients of later steps by their global norm, through a clip buffer (None: off)."""
+        ma_plan_set_clip(self.handle, clip, max_norm, scale)
+        self.clip = clip  # keeps the buffer alive
 
     @property
     def launches(self) -> int:
@@ -535,6 +642,7 @@ class MuonAdamW:
         self._ws_cap = ws_cap
         self._plan = None
         self._grad_ptrs = None
+        self._clip = None
         kinds = ma_partition([self._desc(p, role, grp, None) for p, role, grp in self.entries])
         for (p, role, grp), kind in zip(self.entries, kinds):
             s0 = torch.zeros_like(p)
@@ -573,19 +681,41 @@ class MuonAdamW:
             if g.kind == MA_ADAMW:
                 g.adamw.step = self.step_count
 
-    def step(self, grads=None, stream=None, graph: bool = False) -> None:
-        """One step. graph=True replays the step from a CUDA graph that the plan
+    def _set_clip(self, max_norm, grad_scale):
+        if max_norm is None and grad_scale == 1.0:
+            self._plan.set_clip(None)
+            return
+        if self._clip is None:
+            self._clip = clip_buffer(self.entries[0][0].device)
+        self._plan.set_clip(self._clip, math.inf if max_norm is None else max_norm, grad_scale)
+
+    @property
+    def grad_norm(self):
+        """Global gradient norm (times grad_scale) of the last step that had one, as a 0-d device tensor that the
+        next such step overwrites. Infinite or NaN: that step took every gradient as zero."""
+        if self._clip is None:
+            raise RuntimeError("no step with max_norm or grad_scale yet")
+        return self._clip[0]
+
+    def step(self, grads=None, stream=None, graph: bool = False, max_norm: float | None = None,
+             grad_scale: float = 1.0) -> None:
+        """One step. max_norm: clip the gradients to this global norm; grad_scale: what they have to be multiplied by
+        first (1 / loss scale). Both are applied as the step reads the gradients, which stay as they are; a norm that
+        is not finite makes it a step with zero gradients (see grad_norm). graph=True replays the step from a CUDA graph that the plan
         captures on first use (same results; one launch instead of one per kernel).
         A plan, and with it the graph, belongs to one set of gradient buffers:
         keep them at fixed addresses (as persistent ``.grad`` tensors are)."""
         if grads is None:
             grads = [p.grad for p, _, _ in self.entries]
         self._ensure_plan(grads)
+        self._set_clip(max_norm, grad_scale)
         self._advance()
         self._plan.step(self.groups, stream, graph)
 
-    def step_from_host(self, host_grads, device_grads, stream=None, copy_stream=None) -> None:
-        """One step whose gradients arrive from host memory.
+    def step_from_host(self, host_grads, device_grads, stream=None, copy_stream=None,
+                       max_norm: float | None = None, grad_scale: float = 1.0) -> None:
+        """One step whose gradients arrive from host memory. With max_norm or grad_scale (as in step) the
+        updates start after the last copy, since the norm needs every gradient.
 
         host_grads: pinned CPU tensors (or host pointers), one per entry.
         device_grads: the device buffers that receive them (same shapes and
@@ -604,6 +734,7 @@ class MuonAdamW:
             if getattr(self, "_copy_stream", None) is None:
                 self._copy_stream = torch.cuda.Stream(device=self.entries[0][0].device)
             copy_stream = self._copy_stream
+        self._set_clip(max_norm, grad_scale)
         self._advance()
         self._plan.step_from_host(host_grads, self.groups, stream, copy_stream)
         cs = copy_stream if isinstance(copy_stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(copy_stream))

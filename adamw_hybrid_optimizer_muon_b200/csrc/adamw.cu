@@ -11,7 +11,10 @@
 // fp32. Each block owns one 8192-element chunk of one tensor. It finds the
 // tensor by binary search over the chunk prefix in the parameter block, then
 // streams the chunk with 16-byte loads and stores (4 elements per thread per
-// iteration), so one launch covers every AdamW tensor of a step.
+// iteration), so one launch covers every AdamW tensor of a step. With clipping
+// the gradient is multiplied, as it is read, by the coefficient that the norm
+// pass left on the device: clipping then costs no pass of its own.
+#include "clip.cuh"
 #include "common.cuh"
 #include "internal.h"
 
@@ -47,6 +50,7 @@ __device__ __forceinline__ float load_g1(const void* g, int gdt, int64_t i) {
     return reinterpret_cast<const float*>(g)[i];
 }
 
+template <bool CLIP>
 __global__ void __launch_bounds__(256) adamw_kernel(const __grid_constant__ AdamwLaunch L) {
     griddep_launch_dependents();
     griddep_wait();
@@ -59,6 +63,7 @@ __global__ void __launch_bounds__(256) adamw_kernel(const __grid_constant__ Adam
     }
     const AdamwTensorDesc& T = L.t[lo];
     const AdamwGroupConst H = L.grp[T.group];
+    const float coef = CLIP ? L.clip->coef : 1.f;
     const int64_t start = (chunk - T.chunk0) * kAdamwChunk;
     if (start >= T.numel) return;
     const int64_t end = min(start + (int64_t)kAdamwChunk, T.numel);
@@ -74,6 +79,10 @@ __global__ void __launch_bounds__(256) adamw_kernel(const __grid_constant__ Adam
             float4 v = *reinterpret_cast<const float4*>(T.v + i);
             float g[4];
             load_g4(T.g, L.gdt, i, g);
+            if (CLIP) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) g[k] = clip_value(g[k], coef);
+            }
             adamw_elem(p.x, m.x, v.x, g[0], H);
             adamw_elem(p.y, m.y, v.y, g[1], H);
             adamw_elem(p.z, m.z, v.z, g[2], H);
@@ -87,7 +96,8 @@ __global__ void __launch_bounds__(256) adamw_kernel(const __grid_constant__ Adam
     for (int64_t i = scalar_from + threadIdx.x; i < end; i += 256) {
         if (!MA_INB(i, 1, T.numel, L.status)) continue;
         float p = T.p[i], m = T.m[i], v = T.v[i];
-        adamw_elem(p, m, v, load_g1(T.g, L.gdt, i), H);
+        const float g = load_g1(T.g, L.gdt, i);
+        adamw_elem(p, m, v, CLIP ? clip_value(g, coef) : g, H);
         T.p[i] = p;
         T.m[i] = m;
         T.v[i] = v;
@@ -96,11 +106,16 @@ __global__ void __launch_bounds__(256) adamw_kernel(const __grid_constant__ Adam
 
 }  // namespace
 
-const void* adamw_kernel_func() { return reinterpret_cast<const void*>(adamw_kernel); }
+bool is_adamw_kernel(const void* func) {
+    return func == reinterpret_cast<const void*>(adamw_kernel<false>) ||
+           func == reinterpret_cast<const void*>(adamw_kernel<true>);
+}
 
 cudaError_t launch_adamw(const AdamwLaunch& L, cudaStream_t s) {
     if (L.nchunks <= 0 || L.ntensors <= 0) return cudaSuccess;
-    return launch_pdl(adamw_kernel, dim3((unsigned)L.nchunks), dim3(256), 0, s, L);
+    const dim3 grid((unsigned)L.nchunks);
+    return L.clip ? launch_pdl(adamw_kernel<true>, grid, dim3(256), 0, s, L)
+                  : launch_pdl(adamw_kernel<false>, grid, dim3(256), 0, s, L);
 }
 
 }  // namespace ma

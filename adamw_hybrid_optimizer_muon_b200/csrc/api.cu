@@ -69,6 +69,8 @@ thread_local bool g_prof_on = false;
 thread_local std::vector<std::pair<cudaEvent_t, cudaEvent_t>> g_prof_pool;
 thread_local std::vector<ProfRec> g_prof_recs;
 
+}  // namespace
+
 // Returns the record index, or -1 when profiling is off or an event is unavailable.
 int prof_begin(int cls, cudaStream_t s) {
     if (!g_prof_on) return -1;
@@ -94,6 +96,8 @@ void prof_end(int rec, cudaStream_t s, double flops, double bytes) {
     r.bytes = bytes;
     cudaEventRecord(g_prof_pool[r.ev].second, s);
 }
+
+namespace {
 
 constexpr size_t kAlign = 256;
 // Muon sub-batch sizes when gradients stream in from the host: the first
@@ -140,6 +144,12 @@ int device_ok_and_sms(int* sms) {
     if (sms) *sms = v;
     return MA_OK;
 }
+
+}  // namespace
+
+int device_ready(int* sms) { return device_ok_and_sms(sms); }
+
+namespace {
 
 // ------------------------------------------------------------------ Muon geometry
 
@@ -280,6 +290,7 @@ struct MuonJob {
     float* const* M;
     const ma_muon_hparams_t* hp;
     uint8_t* ws;
+    const ClipHead* clip;  // coefficient of the gradients, or NULL
 };
 
 // Bit k set: Newton-Schulz iteration k has c != 0 (it needs the A^2 term).
@@ -320,6 +331,7 @@ int muon_prep(const MuonJob& j, cudaStream_t s, int max_blocks, bool side, int* 
     P.tiles_c = (g.C + kPrepTCols - 1) / kPrepTCols;
     P.beta = hp.beta;
     P.omb = 1.f - hp.beta;
+    P.clip = j.clip;
     P.X = j.ws + g.off_x0;
     P.partials = part;
     for (int b = 0; b < j.batch; ++b) {
@@ -587,8 +599,8 @@ int run_muon_jobs(const MuonJob* jobs, int njobs, cudaStream_t s, int sms, int* 
 
 // One batch with workspace ws.
 int run_muon(int batch, const MuonGeom& g, float* const* W, const void* const* G, int gdt, float* const* M,
-             const ma_muon_hparams_t& hp, void* ws, cudaStream_t s, int sms, int* launches) {
-    const MuonJob j{batch, g, W, G, gdt, M, &hp, reinterpret_cast<uint8_t*>(ws)};
+             const ma_muon_hparams_t& hp, const ClipHead* clip, void* ws, cudaStream_t s, int sms, int* launches) {
+    const MuonJob j{batch, g, W, G, gdt, M, &hp, reinterpret_cast<uint8_t*>(ws), clip};
     return run_muon_jobs(&j, 1, s, sms, launches);
 }
 
@@ -668,13 +680,14 @@ struct AdamwItem {
 };
 
 // Launch AdamW over items (all with gradient dtype gdt) in parameter-block batches.
-int run_adamw(const std::vector<AdamwItem>& items, int gdt, const AdamwGroupConst* grp, int ngroups, cudaStream_t s,
-              int* launches) {
+int run_adamw(const std::vector<AdamwItem>& items, int gdt, const AdamwGroupConst* grp, int ngroups,
+              const ClipHead* clip, cudaStream_t s, int* launches) {
     static thread_local AdamwLaunch L;  // ~19 KB parameter block, copied at launch
     size_t i = 0;
     while (i < items.size()) {
         std::memset(&L, 0, sizeof(L));
         L.gdt = gdt;
+        L.clip = clip;
         L.status = device_status_ptr();
         for (int k = 0; k < ngroups; ++k) L.grp[k] = grp[k];
         int64_t chunk = 0;
@@ -756,6 +769,10 @@ struct ma_plan {
     // segments in turn, so that a segment's momentum pass can run under the
     // chain of the one before it (on the side stream)
     size_t region = 0;
+    // ma_plan_set_clip: the clip buffer (NULL: no clipping) and its parameters
+    ClipArgs clip{nullptr, 1.f, 0.f, 0};
+    bool measure = false;  // fill the buffer in each step (else: take the coef it holds)
+    const ClipHead* clip_head() const { return clip.clip ? clip.head() : nullptr; }
     int last_launches = 0;
     std::vector<cudaEvent_t> events;  // segment-ready events of muonadamw_step_from_host
     cudaStream_t side = nullptr;      // the momentum passes that run under a chain
@@ -767,7 +784,7 @@ struct ma_plan {
         cudaGraphNode_t node;
         cudaKernelNodeParams params;  // func, launch shape; kernelParams replaced on update
         std::vector<uint8_t> arg;     // the kernel's single by-value parameter
-        int final_apply;              // 0: AdamW launch, 1: Newton-Schulz final apply
+        int kind;                     // 0: AdamW launch, 1: Newton-Schulz final apply, 2: clip finalize
     };
     struct Graph {
         cudaGraph_t graph = nullptr;
@@ -943,6 +960,7 @@ void build_jobs(const ma_plan* plan, const ma_group_t* groups, const Segment& sg
         J.gdt = plan->t[b.members[0]].grad_dtype;
         J.hp = &hp;
         J.ws = base;
+        J.clip = plan->clip_head();
         base += J.g.total;  // a multiple of the workspace alignment
         const size_t off = out.W.size();
         for (int k = 0; k < pt.count; ++k) {
@@ -972,7 +990,7 @@ int run_adamw_segment(ma_plan* plan, const ma_group_t* groups, cudaStream_t s, i
             if (x.grad_dtype != dt) continue;
             items.push_back({x.param, x.grad, x.state0, x.state1, tensor_numel(x), x.group});
         }
-        if (!items.empty() && (st = run_adamw(items, dt, gc, ngroups, s, launches))) return st;
+        if (!items.empty() && (st = run_adamw(items, dt, gc, ngroups, plan->clip_head(), s, launches))) return st;
     }
     return MA_OK;
 }
@@ -1021,6 +1039,15 @@ int side_resources(ma_plan* plan, int dev, size_t nevents, cudaStream_t* side) {
     return MA_OK;
 }
 
+// The global norm of every planned gradient, into the plan's clip buffer.
+int run_clip(ma_plan* plan, cudaStream_t s, int sms, int* launches) {
+    NvtxRange range("ma.clip");
+    std::vector<GradItem> items;
+    for (const ma_tensor_t& x : plan->t)
+        if (const int64_t n = tensor_numel(x)) items.push_back({x.grad, n, x.grad_dtype});
+    return cuda_status(launch_grad_clip(items, plan->clip, sms, false, s, launches));
+}
+
 // One step over segments, on stream s. ready (may be null): per segment, an
 // event its work must wait for (the host copies of its gradients).
 //
@@ -1055,6 +1082,12 @@ int run_segments(ma_plan* plan, const ma_group_t* groups, const std::vector<Segm
     cudaStream_t side = nullptr;
     cudaEvent_t *ev_fork = nullptr, *ev_prep = nullptr, *ev_chain = nullptr;
     int st;
+    if (plan->clip.clip && plan->measure) {
+        // the norm reads every gradient before anything uses one: all copies first
+        for (size_t k = 0; ready && k < segs.size(); ++k)
+            if (cudaStreamWaitEvent(s, ready[k], 0) != cudaSuccess) return MA_ERR_CUDA;
+        if ((st = run_clip(plan, s, sms, launches))) return st;
+    }
     if (any_side) {
         int dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess) return MA_ERR_CUDA;
@@ -1389,9 +1422,16 @@ size_t muon_workspace_bytes(int batch, int64_t R, int64_t C, const ma_muon_hpara
 
 int muon_step_batched(int batch, int64_t R, int64_t C, float* const* W, const void* const* G, int gdt,
                       float* const* M, const ma_muon_hparams_t* hp, void* ws, size_t ws_bytes, void* stream) {
+    return muon_step_batched_clipped(batch, R, C, W, G, gdt, M, hp, nullptr, ws, ws_bytes, stream);
+}
+
+int muon_step_batched_clipped(int batch, int64_t R, int64_t C, float* const* W, const void* const* G, int gdt,
+                              float* const* M, const ma_muon_hparams_t* hp, const void* clip, void* ws,
+                              size_t ws_bytes, void* stream) {
     MuonGeom g;
     int st = check_muon_call(batch, R, C, W, G, gdt, M, hp, &g);
     if (st) return st;
+    if (!aligned(clip, kAlign)) return MA_ERR_ALIGN;
     if (g.total == 0) return MA_OK;
     if (!ws || !aligned(ws, kAlign) || ws_bytes < g.total) return MA_ERR_WORKSPACE;
     int sms = 0;
@@ -1409,8 +1449,9 @@ int muon_step_batched(int batch, int64_t R, int64_t C, float* const* W, const vo
         const int cnt = std::min(sub, batch - s0);
         MuonGeom gc;
         muon_geom(cnt, R, C, *hp, &gc);
-        if ((st = run_muon(cnt, gc, W + s0, G + s0, gdt, M + s0, *hp, ws, reinterpret_cast<cudaStream_t>(stream),
-                           sms, &launches)))
+        if ((st = run_muon(cnt, gc, W + s0, G + s0, gdt, M + s0, *hp,
+                           reinterpret_cast<const ClipHead*>(clip), ws, reinterpret_cast<cudaStream_t>(stream), sms,
+                           &launches)))
             return st;
     }
     return MA_OK;
@@ -1494,10 +1535,16 @@ int ns_iterate_bf16(int batch, int64_t m, int64_t n, const uint16_t* X_in, uint1
 
 int adamw_step_fused(int n, float* const* P, const void* const* G, int gdt, float* const* M, float* const* V,
                      const int64_t* numel, const ma_adamw_hparams_t* hp, void* stream) {
+    return adamw_step_fused_clipped(n, P, G, gdt, M, V, numel, hp, nullptr, stream);
+}
+
+int adamw_step_fused_clipped(int n, float* const* P, const void* const* G, int gdt, float* const* M, float* const* V,
+                             const int64_t* numel, const ma_adamw_hparams_t* hp, const void* clip, void* stream) {
     if (n < 0) return MA_ERR_SHAPE;
     int st = check_adamw_hp(hp);
     if (st) return st;
     if (gdt != MA_F32 && gdt != MA_BF16) return MA_ERR_DTYPE;
+    if (!aligned(clip, kAlign)) return MA_ERR_ALIGN;
     if (n == 0) return MA_OK;
     if (!P || !G || !M || !V || !numel) return MA_ERR_NULL;
     std::vector<AdamwItem> items;
@@ -1520,7 +1567,8 @@ int adamw_step_fused(int n, float* const* P, const void* const* G, int gdt, floa
     if ((st = device_ok_and_sms(nullptr))) return st;
     AdamwGroupConst c = adamw_const(*hp);
     int launches = 0;
-    return run_adamw(items, gdt, &c, 1, reinterpret_cast<cudaStream_t>(stream), &launches);
+    return run_adamw(items, gdt, &c, 1, reinterpret_cast<const ClipHead*>(clip),
+                     reinterpret_cast<cudaStream_t>(stream), &launches);
 }
 
 int ma_plan_create(const ma_tensor_t* t, int n, const ma_group_t* groups, int ngroups, ma_plan_t** out,
@@ -1664,6 +1712,32 @@ int ma_plan_create(const ma_tensor_t* t, int n, const ma_group_t* groups, int ng
     return MA_OK;
 }
 
+int ma_plan_set_clip(ma_plan_t* plan, int measure, float scale, float max_norm, void* clip) {
+    if (!plan) return MA_ERR_NULL;
+    if (clip) {
+        if (measure != 0 && measure != 1) return MA_ERR_ARG;
+        if (!(scale > 0.f) || !std::isfinite(scale) || !(max_norm >= 0.f)) return MA_ERR_ARG;
+        if (!aligned(clip, kAlign)) return MA_ERR_ALIGN;
+        const uintptr_t c0 = reinterpret_cast<uintptr_t>(clip), c1 = c0 + MA_CLIP_BYTES;
+        for (size_t i = 0; i < plan->t.size(); ++i) {
+            const ma_tensor_t& x = plan->t[i];
+            const uintptr_t n = (uintptr_t)tensor_numel(x);
+            auto meets = [&](const void* p, uintptr_t bytes) {
+                const uintptr_t a = reinterpret_cast<uintptr_t>(p);
+                return p && a < c1 && c0 < a + bytes;
+            };
+            if (meets(x.param, 4 * n) || meets(x.state0, 4 * n) || meets(x.grad, (x.grad_dtype == MA_BF16 ? 2 : 4) * n) ||
+                (plan->kind[i] == MA_ADAMW && meets(x.state1, 4 * n)))
+                return MA_ERR_ARG;
+        }
+        plan->clip = ClipArgs{clip, scale, max_norm, 0};
+        plan->measure = measure != 0;
+    } else {
+        plan->clip.clip = nullptr;
+    }
+    return MA_OK;
+}
+
 int muonadamw_step(ma_plan_t* plan, const ma_group_t* groups, void* ws, size_t ws_bytes, void* stream) {
     ma::NvtxRange range("ma.step");
     int sms = 0;
@@ -1685,8 +1759,9 @@ namespace {
 
 // What a captured step depends on beyond the per-step values that are patched
 // into its nodes (AdamW hyperparameters and step, Muon lr and weight decay on
-// the tensor-core path): the workspace, the device and the rest of every Muon
-// group's hyperparameters.
+// the tensor-core path, the clipping's scale and largest norm): the workspace,
+// the device, the clip buffer and the rest of every Muon group's
+// hyperparameters.
 std::vector<uint8_t> graph_key(const ma_plan* plan, const ma_group_t* groups, const void* ws, int dev) {
     std::vector<uint8_t> k;
     auto put = [&k](const void* p, size_t n) {
@@ -1695,6 +1770,8 @@ std::vector<uint8_t> graph_key(const ma_plan* plan, const ma_group_t* groups, co
     };
     put(&ws, sizeof(ws));
     put(&dev, sizeof(dev));
+    put(&plan->clip.clip, sizeof(plan->clip.clip));
+    put(&plan->measure, sizeof(plan->measure));
     for (size_t i = 0; i < plan->group_kind.size(); ++i) {
         put(&groups[i].kind, sizeof(groups[i].kind));
         if (groups[i].kind != MA_MUON) continue;
@@ -1734,7 +1811,7 @@ int patch_final_job(void* ctx, const float* W, int64_t Rh, int64_t C, float* dec
     return MA_OK;
 }
 
-// Write this step's hyperparameters into the captured AdamW and final-apply nodes.
+// Write this step's hyperparameters into the captured AdamW, final-apply and clip-finalize nodes.
 int graph_patch(ma_plan* plan, const ma_group_t* groups) {
     const int ngroups = (int)plan->group_kind.size();
     AdamwGroupConst gc[MA_MAX_GROUPS];
@@ -1745,9 +1822,13 @@ int graph_patch(ma_plan* plan, const ma_group_t* groups) {
     for (size_t i = 0; i < plan->t.size(); ++i)
         if (plan->kind[i] == MA_MUON) ctx.tensor_of[plan->t[i].param] = (int)i;
     for (ma_plan::GraphNode& n : plan->g.nodes) {
-        if (n.final_apply == 1) {
+        if (n.kind == 1) {
             const int st = ns_tc_patch_final(n.arg.data(), patch_final_job, &ctx);
             if (st) return st;
+        } else if (n.kind == 2) {
+            ClipFinalize* F = reinterpret_cast<ClipFinalize*>(n.arg.data());
+            F->scale = plan->clip.scale;
+            F->max_norm = plan->clip.max_norm;
         } else {
             AdamwLaunch* L = reinterpret_cast<AdamwLaunch*>(n.arg.data());
             for (int k = 0; k < ngroups; ++k) L->grp[k] = gc[k];
@@ -1826,12 +1907,13 @@ int graph_capture(ma_plan* plan, const ma_group_t* groups, void* ws, int sms, in
             G.release();
             return MA_ERR_CUDA;
         }
-        const bool adamw = p.func == adamw_kernel_func();
+        const bool adamw = is_adamw_kernel(p.func);
         const bool fin = ns_tc_is_final(p.func);
-        if (!adamw && !fin) continue;
-        const size_t bytes = adamw ? sizeof(AdamwLaunch) : ns_tc_launch_bytes();
+        const bool clip = p.func == clip_finalize_func();
+        if (!adamw && !fin && !clip) continue;
+        const size_t bytes = adamw ? sizeof(AdamwLaunch) : clip ? sizeof(ClipFinalize) : ns_tc_launch_bytes();
         const uint8_t* a = reinterpret_cast<const uint8_t*>(p.kernelParams[0]);
-        G.nodes.push_back({node, p, std::vector<uint8_t>(a, a + bytes), fin ? 1 : 0});
+        G.nodes.push_back({node, p, std::vector<uint8_t>(a, a + bytes), fin ? 1 : clip ? 2 : 0});
     }
     G.launches = launches;
     ++G.captures;
@@ -2100,5 +2182,5 @@ extern "C" int muon_step_batched_noalloc(int batch, int64_t R, int64_t C, float*
     void* scratch = noalloc_scratch_ptr();
     if (!scratch) return MA_ERR_CUDA;
     int launches = 0;
-    return run_muon(batch, g, W, G, gdt, M, *hp, scratch, reinterpret_cast<cudaStream_t>(stream), sms, &launches);
+    return run_muon(batch, g, W, G, gdt, M, *hp, nullptr, scratch, reinterpret_cast<cudaStream_t>(stream), sms, &launches);
 }

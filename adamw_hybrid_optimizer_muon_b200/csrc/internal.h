@@ -11,6 +11,7 @@
 
 #include <atomic>
 #include <mutex>
+#include <vector>
 
 #include "../../include/muonadamw.h"
 
@@ -54,6 +55,61 @@ class PerDevice {
     T val_[kMaxDevices];
 };
 
+// Runs a C entry point's body; an exception (host memory that ran out) becomes a status.
+template <typename F>
+int ma_guard(F f) {
+    try {
+        return f();
+    } catch (...) {
+        return MA_ERR_UNSUPPORTED;
+    }
+}
+
+// Launch profiler (api.cu): brackets a launch with two events when profiling is on.
+int prof_begin(int cls, cudaStream_t s);
+void prof_end(int rec, cudaStream_t s, double flops, double bytes);
+
+// MA_OK and the SM count when the current device can run this library (api.cu).
+int device_ready(int* sms);
+
+// ------------------------------------------------------------------ gradient norm and clipping
+
+constexpr int kClipMaxTensors = 1280;  // parameter-block capacity
+constexpr int kClipMaxParts = (MA_CLIP_BYTES - 256) / 8;  // partial sums a clip buffer holds
+
+// The start of a clip buffer; the partial sums of the norm pass begin at byte 256.
+struct ClipHead {
+    float norm;    // scale * sqrt(sumsq)
+    float coef;    // factor every gradient is multiplied by
+    double sumsq;  // sum of squares of the gradients as they are stored
+};
+
+struct ClipArgs {
+    void* clip;
+    float scale, max_norm;
+    int max_blocks;
+    ClipHead* head() const { return reinterpret_cast<ClipHead*>(clip); }
+    double* partials() const { return reinterpret_cast<double*>(reinterpret_cast<uint8_t*>(clip) + 256); }
+};
+
+struct ClipFinalize {
+    ClipHead* head;
+    const double* partials;
+    int32_t nparts;  // negative: take head->sumsq as it is
+    float scale, max_norm;
+};
+
+struct GradItem {
+    const void* g;
+    int64_t numel;
+    int32_t gdt;
+};
+
+cudaError_t launch_grad_clip(const std::vector<GradItem>& items, const ClipArgs& args, int sms, bool in_place,
+                             cudaStream_t s, int* launches);
+cudaError_t launch_clip_finalize(const ClipArgs& a, int nparts, cudaStream_t s);
+const void* clip_finalize_func();  // the kernel's host-side handle (CUDA-graph node matching)
+
 // ------------------------------------------------------------------ AdamW
 
 constexpr int kAdamwChunk = 8192;              // elements per block
@@ -82,12 +138,13 @@ struct AdamwLaunch {
     int32_t gdt;  // ma_dtype_t of every gradient in this launch
     int64_t nchunks;
     int* status;  // device status word (guarded indexing in debug builds)
+    const ClipHead* clip;  // gradients are taken times its coef; NULL: as they are
     AdamwGroupConst grp[MA_MAX_GROUPS];
     AdamwTensorDesc t[kAdamwMaxTensorsPerLaunch];
 };
 
 cudaError_t launch_adamw(const AdamwLaunch& L, cudaStream_t s);
-const void* adamw_kernel_func();  // the kernel's host-side handle (CUDA-graph node matching)
+bool is_adamw_kernel(const void* func);  // whether a kernel node's function is this kernel (CUDA-graph node matching)
 
 // ------------------------------------------------------------------ Muon: momentum + norm
 
@@ -105,6 +162,7 @@ struct MuonPrepLaunch {
     int64_t parts;        // partial sums per unit
     int64_t tiles_c;      // transposing path: blocks of kPrepTCols columns along C
     float beta, omb;
+    const ClipHead* clip;  // gradients are taken times its coef; NULL: as they are
     void* X;
     double* partials;
     const void* G[MA_MAX_BATCH];

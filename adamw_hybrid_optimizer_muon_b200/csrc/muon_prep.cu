@@ -14,6 +14,9 @@
 // 1/(||u||_F + eps), the Frobenius normalisation that the Newton-Schulz GEMMs
 // fold into their epilogues. The sum is deterministic: no float atomics.
 //
+// With clipping (CLIP) the gradient is multiplied, as it is read, by the
+// coefficient that the global norm pass left on the device.
+//
 // Bytes per element: g 2 (bf16) + m read 4 + m write 4 + X write 2 = 12.
 //
 // Two layouts:
@@ -21,6 +24,7 @@
 //    Each thread streams 8 elements per iteration with 16-byte accesses.
 //  * transposing: the unit is tall (rows > cols), so X = u^T. 64x64 tiles go
 //    through shared memory, and reads and writes are both coalesced.
+#include "clip.cuh"
 #include "common.cuh"
 #include "internal.h"
 
@@ -47,8 +51,8 @@ __device__ __forceinline__ float block_sum(float v, float* red) {
     return t;
 }
 
-template <bool GBF16>
-__device__ __forceinline__ void load_g8(const void* G, int64_t i, float (&g)[8]) {
+template <bool GBF16, bool CLIP>
+__device__ __forceinline__ void load_g8(const void* G, int64_t i, float coef, float (&g)[8]) {
     if (GBF16) {
         const uint4 w = __ldcs(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(G) + i));
         g[0] = bf16_lo(w.x); g[1] = bf16_hi(w.x); g[2] = bf16_lo(w.y); g[3] = bf16_hi(w.y);
@@ -57,6 +61,10 @@ __device__ __forceinline__ void load_g8(const void* G, int64_t i, float (&g)[8])
         const float4* gp = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(G) + i);
         const float4 a = __ldcs(gp), c = __ldcs(gp + 1);
         g[0] = a.x; g[1] = a.y; g[2] = a.z; g[3] = a.w; g[4] = c.x; g[5] = c.y; g[6] = c.z; g[7] = c.w;
+    }
+    if (CLIP) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) g[k] = clip_value(g[k], coef);
     }
 }
 
@@ -94,7 +102,7 @@ __device__ __forceinline__ void store_x8(void* X, int64_t i, const float (&d)[8]
 // returns its sum of squares, accumulated in that order. Loads for a full
 // chunk are all issued before any arithmetic (12 independent 16-byte loads
 // in flight per pass).
-template <bool GBF16, bool XF32>
+template <bool GBF16, bool XF32, bool CLIP>
 __device__ __forceinline__ float prep_flat_pass(const MuonPrepLaunch& L, int u, int64_t part, int vt) {
     constexpr int kIter = kPrepChunk / (8 * 256);
     const int b = u / L.heads, h = u % L.heads;
@@ -109,6 +117,7 @@ __device__ __forceinline__ float prep_flat_pass(const MuonPrepLaunch& L, int u, 
                    : static_cast<void*>(reinterpret_cast<uint16_t*>(L.X) + (int64_t)u * L.x_unit);
     const float beta = L.beta, omb = L.omb;
     const bool nest = L.nesterov != 0;
+    const float coef = CLIP ? L.clip->coef : 1.f;
     // buffer extents for the guarded build: a matrix's G and M, and the workspace's X
     [[maybe_unused]] const int64_t mat_elems = (int64_t)L.heads * unit_elems;
     [[maybe_unused]] const int64_t x_elems = (int64_t)L.batch * L.heads * L.x_unit;
@@ -124,7 +133,7 @@ __device__ __forceinline__ float prep_flat_pass(const MuonPrepLaunch& L, int u, 
 #pragma unroll
             for (int e = 0; e < 8; ++e) g[k][e] = m[k][e] = 0.f;
             if (!ok[k]) continue;
-            load_g8<GBF16>(G, i, g[k]);
+            load_g8<GBF16, CLIP>(G, i, coef, g[k]);
             const float4 a = __ldcs(reinterpret_cast<const float4*>(M + i));
             const float4 c = __ldcs(reinterpret_cast<const float4*>(M + i + 4));
             m[k][0] = a.x; m[k][1] = a.y; m[k][2] = a.z; m[k][3] = a.w;
@@ -144,7 +153,7 @@ __device__ __forceinline__ float prep_flat_pass(const MuonPrepLaunch& L, int u, 
         for (int64_t i = start + 8 * (int64_t)vt; i < end; i += 8 * 256) {
             if (!(MA_INB(off + i, 8, mat_elems, L.status) && MA_INB(xu + i, 8, x_elems, L.status))) continue;
             float g[8], m[8], d[8];
-            load_g8<GBF16>(G, i, g);
+            load_g8<GBF16, CLIP>(G, i, coef, g);
             const float4 a = __ldcs(reinterpret_cast<const float4*>(M + i));
             const float4 c = __ldcs(reinterpret_cast<const float4*>(M + i + 4));
             m[0] = a.x; m[1] = a.y; m[2] = a.z; m[3] = a.w; m[4] = c.x; m[5] = c.y; m[6] = c.z; m[7] = c.w;
@@ -166,13 +175,13 @@ __device__ __forceinline__ float warp_sum(float v) {
 // Flat path, on the caller's stream: one block of 256 threads per chunk of
 // kPrepChunk elements of one unit. The chunk's partial is the sum over the
 // block in a fixed order: each warp's butterfly, then the eight warps in order.
-template <bool GBF16, bool XF32>
+template <bool GBF16, bool XF32, bool CLIP>
 __global__ void __launch_bounds__(256) prep_flat_kernel(const __grid_constant__ MuonPrepLaunch L) {
     griddep_launch_dependents();
     griddep_wait();
     __shared__ float red[8];
     const int u = blockIdx.y;
-    const float s = warp_sum(prep_flat_pass<GBF16, XF32>(L, u, blockIdx.x, threadIdx.x));
+    const float s = warp_sum(prep_flat_pass<GBF16, XF32, CLIP>(L, u, blockIdx.x, threadIdx.x));
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = s;
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -191,7 +200,7 @@ __global__ void __launch_bounds__(256) prep_flat_kernel(const __grid_constant__ 
 // other) and keeps their sums apart, and the warps' butterflies and the final
 // sum run in prep_flat_kernel's order: every partial, and so every scale, is
 // the same bits on either path.
-template <bool GBF16, bool XF32>
+template <bool GBF16, bool XF32, bool CLIP>
 __global__ void __launch_bounds__(kPrepSideThreads, 6) prep_flat_side_kernel(const __grid_constant__ MuonPrepLaunch L) {
     griddep_launch_dependents();
     griddep_wait();
@@ -201,8 +210,8 @@ __global__ void __launch_bounds__(kPrepSideThreads, 6) prep_flat_side_kernel(con
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
         const int u = (int)(it / L.parts);
         const int64_t part = it - (int64_t)u * L.parts;
-        const float lo = warp_sum(prep_flat_pass<GBF16, XF32>(L, u, part, threadIdx.x));        // warps 0..3
-        const float hi = warp_sum(prep_flat_pass<GBF16, XF32>(L, u, part, threadIdx.x + 128));  // warps 4..7
+        const float lo = warp_sum(prep_flat_pass<GBF16, XF32, CLIP>(L, u, part, threadIdx.x));        // warps 0..3
+        const float hi = warp_sum(prep_flat_pass<GBF16, XF32, CLIP>(L, u, part, threadIdx.x + 128));  // warps 4..7
         if ((threadIdx.x & 31) == 0) {
             red[w] = lo;
             red[4 + w] = hi;
@@ -232,7 +241,7 @@ __global__ void __launch_bounds__(kPrepSideThreads, 6) prep_flat_side_kernel(con
 // block per pair on the caller's stream, or a small grid on a side stream,
 // where a block (at most 80 registers a thread, 16 bytes of shared memory)
 // fits beside a Newton-Schulz CTA. The partials do not depend on the grid.
-template <bool GBF16, bool XF32>
+template <bool GBF16, bool XF32, bool CLIP>
 __global__ void __launch_bounds__(kPrepSideThreads, 6) prep_transpose_kernel(const __grid_constant__ MuonPrepLaunch L) {
     griddep_launch_dependents();
     griddep_wait();
@@ -245,6 +254,7 @@ __global__ void __launch_bounds__(kPrepSideThreads, 6) prep_transpose_kernel(con
     const int64_t items = (int64_t)L.batch * L.heads * L.parts;
     const float beta = L.beta, omb = L.omb;
     const bool nest = L.nesterov != 0;
+    const float coef = CLIP ? L.clip->coef : 1.f;
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
         const int u = (int)(it / L.parts);
         const int64_t part = it - (int64_t)u * L.parts;
@@ -287,8 +297,12 @@ __global__ void __launch_bounds__(kPrepSideThreads, 6) prep_transpose_kernel(con
 #pragma unroll
             for (int i = i0; i < i0 + RB; ++i) {
                 if (i < rows && MA_INB(e0 + (int64_t)i * L.C, 2, mat_elems, L.status)) {
-                    const float g0 = GBF16 ? bf16_lo(g[i - i0][0]) : __uint_as_float(g[i - i0][0]);
-                    const float g1 = GBF16 ? bf16_hi(g[i - i0][0]) : __uint_as_float(g[i - i0][GW - 1]);
+                    float g0 = GBF16 ? bf16_lo(g[i - i0][0]) : __uint_as_float(g[i - i0][0]);
+                    float g1 = GBF16 ? bf16_hi(g[i - i0][0]) : __uint_as_float(g[i - i0][GW - 1]);
+                    if (CLIP) {
+                        g0 = clip_value(g0, coef);
+                        g1 = clip_value(g1, coef);
+                    }
                     const float mn0 = beta * d[i][0] + omb * g0;
                     const float mn1 = beta * d[i][1] + omb * g1;
                     d[i][0] = nest ? beta * mn0 + omb * g0 : mn0;
@@ -362,6 +376,38 @@ int64_t prep_parts_per_unit(int64_t Rh, int64_t C, int transposed) {
     return (Rh * C + kPrepChunk - 1) / kPrepChunk;
 }
 
+namespace {
+
+template <bool GB, bool XF, bool CLIP>
+const void* side_func() {
+    return reinterpret_cast<const void*>(prep_flat_side_kernel<GB, XF, CLIP>);
+}
+
+template <bool GB, bool XF, bool CLIP>
+const void* transpose_func() {
+    return reinterpret_cast<const void*>(prep_transpose_kernel<GB, XF, CLIP>);
+}
+
+// Compile-time choices of a momentum kernel: bf16 gradients, fp32 X, clipping.
+template <bool GB, bool XF, bool CLIP>
+struct Types {
+    static constexpr bool gb = GB, xf = XF, clip = CLIP;
+};
+
+// f(Types<...>{}) for a launch's types.
+template <typename F>
+cudaError_t with_types(const MuonPrepLaunch& L, F f) {
+    const bool gb = L.gdt == MA_BF16, xf = L.x_f32 != 0;
+    if (L.clip) {
+        if (gb) return xf ? f(Types<true, true, true>{}) : f(Types<true, false, true>{});
+        return xf ? f(Types<false, true, true>{}) : f(Types<false, false, true>{});
+    }
+    if (gb) return xf ? f(Types<true, true, false>{}) : f(Types<true, false, false>{});
+    return xf ? f(Types<false, true, false>{}) : f(Types<false, false, false>{});
+}
+
+}  // namespace
+
 // The kernels that run beside Newton-Schulz CTAs prefer the largest
 // shared-memory carveout, the one those CTAs set on their SMs, so that their
 // blocks can join those SMs.
@@ -374,14 +420,14 @@ cudaError_t prep_setup() {
     if (e != cudaSuccess) return e;
     int done = 0;
     return cache.get(dev, &done, [](int* v) -> cudaError_t {
-        const void* fns[8] = {reinterpret_cast<const void*>(prep_flat_side_kernel<true, false>),
-                              reinterpret_cast<const void*>(prep_flat_side_kernel<true, true>),
-                              reinterpret_cast<const void*>(prep_flat_side_kernel<false, false>),
-                              reinterpret_cast<const void*>(prep_flat_side_kernel<false, true>),
-                              reinterpret_cast<const void*>(prep_transpose_kernel<true, false>),
-                              reinterpret_cast<const void*>(prep_transpose_kernel<true, true>),
-                              reinterpret_cast<const void*>(prep_transpose_kernel<false, false>),
-                              reinterpret_cast<const void*>(prep_transpose_kernel<false, true>)};
+        const void* fns[16] = {
+            side_func<true, false, false>(),  side_func<true, true, false>(),  side_func<false, false, false>(),
+            side_func<false, true, false>(),  side_func<true, false, true>(),  side_func<true, true, true>(),
+            side_func<false, false, true>(),  side_func<false, true, true>(),  transpose_func<true, false, false>(),
+            transpose_func<true, true, false>(),  transpose_func<false, false, false>(),
+            transpose_func<false, true, false>(), transpose_func<true, false, true>(),
+            transpose_func<true, true, true>(),   transpose_func<false, false, true>(),
+            transpose_func<false, true, true>()};
         for (const void* f : fns) {
             const cudaError_t r = cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,
                                                        cudaSharedmemCarveoutMaxShared);
@@ -395,35 +441,24 @@ cudaError_t prep_setup() {
 cudaError_t launch_muon_prep(const MuonPrepLaunch& L, int max_blocks, cudaStream_t s) {
     const int units = L.batch * L.heads;
     if (units == 0 || L.parts == 0) return cudaSuccess;
-    const bool gb = L.gdt == MA_BF16, xf = L.x_f32 != 0;
     cudaError_t e;
-    if (L.transposed) {
-        if ((e = prep_setup()) != cudaSuccess) return e;
-        int64_t items = (int64_t)units * L.parts;
-        if (max_blocks > 0 && items > max_blocks) items = max_blocks;
-        if (items > INT32_MAX) items = INT32_MAX;
-        const dim3 grid((unsigned)items), block(kPrepSideThreads);
-        if (gb && !xf) e = launch_pdl(prep_transpose_kernel<true, false>, grid, block, 0, s, L);
-        else if (gb) e = launch_pdl(prep_transpose_kernel<true, true>, grid, block, 0, s, L);
-        else if (!xf) e = launch_pdl(prep_transpose_kernel<false, false>, grid, block, 0, s, L);
-        else e = launch_pdl(prep_transpose_kernel<false, true>, grid, block, 0, s, L);
-    } else if (max_blocks <= 0) {
+    if (!L.transposed && max_blocks <= 0) {
         const dim3 grid((unsigned)L.parts, (unsigned)units);
-        if (gb && !xf) e = launch_pdl(prep_flat_kernel<true, false>, grid, dim3(256), 0, s, L);
-        else if (gb) e = launch_pdl(prep_flat_kernel<true, true>, grid, dim3(256), 0, s, L);
-        else if (!xf) e = launch_pdl(prep_flat_kernel<false, false>, grid, dim3(256), 0, s, L);
-        else e = launch_pdl(prep_flat_kernel<false, true>, grid, dim3(256), 0, s, L);
-    } else {
-        if ((e = prep_setup()) != cudaSuccess) return e;
-        int64_t items = (int64_t)units * L.parts;
-        if (items > max_blocks) items = max_blocks;
-        const dim3 grid((unsigned)items), block(kPrepSideThreads);
-        if (gb && !xf) e = launch_pdl(prep_flat_side_kernel<true, false>, grid, block, 0, s, L);
-        else if (gb) e = launch_pdl(prep_flat_side_kernel<true, true>, grid, block, 0, s, L);
-        else if (!xf) e = launch_pdl(prep_flat_side_kernel<false, false>, grid, block, 0, s, L);
-        else e = launch_pdl(prep_flat_side_kernel<false, true>, grid, block, 0, s, L);
+        return with_types(L, [&](auto t) {
+            using T = decltype(t);
+            return launch_pdl(prep_flat_kernel<T::gb, T::xf, T::clip>, grid, dim3(256), 0, s, L);
+        });
     }
-    return e;
+    if ((e = prep_setup()) != cudaSuccess) return e;
+    int64_t items = (int64_t)units * L.parts;
+    if (max_blocks > 0 && items > max_blocks) items = max_blocks;
+    if (items > INT32_MAX) items = INT32_MAX;
+    const dim3 grid((unsigned)items), block(kPrepSideThreads);
+    return with_types(L, [&](auto t) {
+        using T = decltype(t);
+        return L.transposed ? launch_pdl(prep_transpose_kernel<T::gb, T::xf, T::clip>, grid, block, 0, s, L)
+                            : launch_pdl(prep_flat_side_kernel<T::gb, T::xf, T::clip>, grid, block, 0, s, L);
+    });
 }
 
 cudaError_t launch_norm_finalize(const double* partials, int64_t parts, int units, float eps, float* scale,

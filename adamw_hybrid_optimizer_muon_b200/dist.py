@@ -33,13 +33,15 @@ the library's kernels. Tests on CPU ranks replace ``_local_step``.
 from __future__ import annotations
 
 import hashlib
+import math
 from dataclasses import dataclass, field
 
 import torch
 import torch.distributed as dist
 
-from . import (MA_ADAMW, MA_MUON, ROLE_HIDDEN, Tensor, _dtype_code, _ptr, group_table, lib, ma_partition,
-               ma_plan_create, ma_plan_destroy, ma_shard_layout, muonadamw_step)
+from . import (CLIP_BYTES, MA_ADAMW, MA_MUON, ROLE_HIDDEN, Tensor, _dtype_code, _ptr, group_table, lib,
+               ma_clip_finalize, ma_grad_norm, ma_partition, ma_plan_create, ma_plan_destroy, ma_plan_set_clip,
+               ma_shard_layout, muonadamw_step)
 
 __all__ = ["DistMuonAdamW", "Piece", "ShardBucketView"]
 
@@ -174,6 +176,8 @@ class DistMuonAdamW:
                                    self.grad_shard[r0:r1].view(shape), self.state0[r0:r1].view(shape), s1))
         self._plans = None
         self._ws = None
+        self._clip = None       # clip buffer, once a step asked for the global norm
+        self._clipping = False  # whether the current step takes its coefficient
         self._side = None   # stream the reductions are issued from (CUDA only)
 
     # ------------------------------------------------------------------ step
@@ -213,13 +217,37 @@ class DistMuonAdamW:
             self._build_plans()
         plan = self._plans[b]
         if plan is not None:
+            ma_plan_set_clip(plan, self._clip if self._clipping else None, measure=False)
             muonadamw_step(plan, self.groups, self._ws, self._ws.numel())
 
-    def step(self) -> None:
-        """One data-parallel step: reduce-scatter, local update, all-gather (all asynchronous on the device)."""
-        self._run(None)
+    def _local_sumsq(self) -> None:
+        """Sum of squares of this rank's reduced gradients, into the clip buffer."""
+        ma_grad_norm([pc.grad for pc in self.pieces()], self._clip)
 
-    def step_from_host(self, host_flat: torch.Tensor) -> None:
+    def _finish_norm(self, max_norm: float, grad_scale: float) -> None:
+        """Norm and coefficient from the clip buffer's sum of squares."""
+        ma_clip_finalize(self._clip, max_norm, grad_scale)
+
+    @property
+    def grad_norm(self) -> torch.Tensor:
+        """Global norm of the averaged gradients (times grad_scale) of the last step that had one, the same on every
+        rank: a 0-d tensor on the device that the next such step overwrites. Infinite or NaN: that step took every
+        gradient as zero."""
+        if self._clip is None:
+            raise RuntimeError("no step with max_norm or grad_scale yet")
+        return self._clip[0]
+
+    def step(self, max_norm: float | None = None, grad_scale: float = 1.0) -> None:
+        """One data-parallel step: reduce-scatter, local update, all-gather (all asynchronous on the device).
+
+        max_norm clips the averaged gradients to this global norm, and grad_scale is what they have to be
+        multiplied by first: each rank sums the squares of its own share, the sums are added over the ranks, and
+        the updates take the gradients times the resulting factor. The first update then waits for the last
+        bucket's reduction (the norm needs every gradient); the all-gathers still overlap the updates."""
+        self._run(None, max_norm, grad_scale)
+
+    def step_from_host(self, host_flat: torch.Tensor, max_norm: float | None = None,
+                       grad_scale: float = 1.0) -> None:
         """One step whose gradients come from ``host_flat``, a pinned CPU tensor
         shaped and typed like ``flat_grad`` (``host_views`` gives its per-tensor
         views). Each bucket's gradients are copied on a side stream and that
@@ -229,16 +257,23 @@ class DistMuonAdamW:
         The call returns before the copies have read ``host_flat``: do not
         write to it until ``host_copies_done`` (a CUDA event recorded after the
         last copy) has completed, e.g. ``opt.host_copies_done.synchronize()``,
-        or the step may read the new values for some buckets."""
+        or the step may read the new values for some buckets. max_norm and
+        grad_scale are those of :meth:`step`."""
         if host_flat.shape != self.flat_grad.shape or host_flat.dtype != self.flat_grad.dtype:
             raise ValueError("host_flat must match flat_grad in shape and dtype")
-        self._run(host_flat)
+        self._run(host_flat, max_norm, grad_scale)
 
     def host_views(self, host_flat: torch.Tensor) -> list:
         """Per-tensor views of a flat host gradient buffer (same offsets as ``grads``)."""
         return [host_flat[off:off + g.numel()].view(g.shape) for g, (_, _, off) in zip(self.grads, self.slots)]
 
-    def _run(self, host_flat) -> None:
+    def _run(self, host_flat, max_norm, grad_scale) -> None:
+        self._clipping = max_norm is not None or grad_scale != 1.0
+        max_norm = math.inf if max_norm is None else float(max_norm)
+        if not (grad_scale > 0 and math.isfinite(grad_scale) and max_norm >= 0):
+            raise ValueError("max_norm must not be negative, and grad_scale must be positive and finite")
+        if self._clipping and self._clip is None:
+            self._clip = torch.zeros(CLIP_BYTES // 4, dtype=torch.float32, device=self.flat_grad.device)
         self._advance()
         cuda = self.flat_grad.is_cuda
         if not cuda and host_flat is not None:
@@ -273,6 +308,14 @@ class DistMuonAdamW:
             # every copy from host_flat is queued on `side` before this event
             self.host_copies_done = torch.cuda.Event()
             self.host_copies_done.record(side)
+        if self._clipping:
+            for b, work in enumerate(reduces):
+                if work is not None:
+                    work.wait()
+                    reduces[b] = None
+            self._local_sumsq()
+            dist.all_reduce(self._clip.view(torch.float64)[1:2], op=dist.ReduceOp.SUM, group=self.pg)
+            self._finish_norm(max_norm, grad_scale)
         gathers = []
         for b, bv in enumerate(self.buckets):
             if reduces[b] is not None:

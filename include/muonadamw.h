@@ -291,6 +291,52 @@ int adamw_step_fused(int n, float* const* P, const void* const* G, int gdt, floa
                      float* const* V, const int64_t* numel, const ma_adamw_hparams_t* hp,
                      void* stream);
 
+/* ---------------------------------------------------------------- gradient norm and clipping */
+
+/* Global gradient norm and clipping. Over n gradients g (fp32 or bf16),
+ *     N    = scale * sqrt(sum over all of g^2)
+ *     coef = scale * min(1, max_norm / N)
+ * and a clipped gradient is coef * g: scaled, and with a norm of at most
+ * max_norm. scale > 0 is what the stored gradients have to be multiplied by
+ * (1 / loss scale, 1 / micro-batches; 1 for none). max_norm >= 0; infinity
+ * measures and scales without clipping. When the sum of squares is not finite
+ * (an infinity or a NaN among the gradients), coef is 0; a gradient times a
+ * coef of 0 is 0 whatever it holds, so that step goes on as with zero
+ * gradients, and norm tells. Squares are summed in fp64 beyond 64 values, and
+ * in fp64 throughout where fp32 would overflow or lose them; the order is
+ * fixed, so the same call on the same GPU model gives the same bits.
+ *
+ * clip: device buffer of MA_CLIP_BYTES, 256-byte aligned, owned by the caller:
+ * bytes 0..3 norm (float, N), 4..7 coef (float), 8..15 the sum of squares of
+ * the stored gradients (double), the rest scratch. It needs no initial value.
+ * Calls that overlap on the GPU (other streams, replays of captured graphs)
+ * need a buffer each.
+ *  G: host array of n device pointers (NULL for an empty tensor); any element
+ *     alignment. gdt: host array of n ma_dtype_t. numel: host array of n counts.
+ * ma_grad_norm fills norm, coef and the sum of squares and leaves the
+ * gradients alone. ma_grad_clip also multiplies them in place, with one
+ * rounding each to their dtype; no gradient may overlap another (MA_ERR_ARG).
+ * A coef of exactly 1 leaves them untouched. ma_clip_finalize forms norm and
+ * coef again from the sum of squares in the buffer: after the sums of several
+ * ranks, each over its own share, were added. */
+#define MA_CLIP_BYTES 16640
+int ma_grad_norm(int n, const void* const* G, const int32_t* gdt, const int64_t* numel, float scale,
+                 float max_norm, void* clip, void* stream);
+int ma_grad_clip(int n, void* const* G, const int32_t* gdt, const int64_t* numel, float scale,
+                 float max_norm, void* clip, void* stream);
+int ma_clip_finalize(float scale, float max_norm, void* clip, void* stream);
+
+/* adamw_step_fused and muon_step_batched on gradients taken times the coef of
+ * a clip buffer (filled by an earlier call on the stream) as they are read: no
+ * pass over the gradients of its own, and the gradients stay as they are.
+ * clip NULL: unclipped, the same bits as the functions without it. */
+int adamw_step_fused_clipped(int n, float* const* P, const void* const* G, int gdt, float* const* M,
+                             float* const* V, const int64_t* numel, const ma_adamw_hparams_t* hp,
+                             const void* clip, void* stream);
+int muon_step_batched_clipped(int batch, int64_t R, int64_t C, float* const* W, const void* const* G,
+                              int gdt, float* const* M, const ma_muon_hparams_t* hp, const void* clip,
+                              void* ws, size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------- whole step */
 
 /* Build a plan for a parameter table [P1 "The MuonAdamW Class Architecture"]:
@@ -313,6 +359,17 @@ int ma_plan_create(const ma_tensor_t* t, int n, const ma_group_t* groups, int ng
  * and the AdamW step counter change here). ws: device, >= the planned size. */
 int muonadamw_step(ma_plan_t* plan, const ma_group_t* groups, void* ws, size_t ws_bytes,
                    void* stream);
+
+/* Clip the gradients of every later step over the plan (muonadamw_step,
+ * _graph and _from_host) by their global norm. measure 1: each step first
+ * fills `clip` (MA_CLIP_BYTES, as above) from all planned gradients, then
+ * takes them times its coef. measure 0: each step takes the coef that the
+ * buffer holds by then (a norm over more than this plan: several plans, several
+ * ranks); scale and max_norm are not used. clip NULL turns it off again. The scale and max_norm may change
+ * from step to step, also of a captured graph; another clip buffer captures
+ * again. A step from host memory then starts its updates after the last copy.
+ * MA_ERR_ARG when clip overlaps a planned buffer. */
+int ma_plan_set_clip(ma_plan_t* plan, int measure, float scale, float max_norm, void* clip);
 
 /* One MuonAdamW step whose gradients start in host memory (for example
  * gradients offloaded to the CPU). host_grads: host array of n pointers, one
@@ -378,7 +435,8 @@ void ma_plan_destroy(ma_plan_t* plan);
                                 /* the Newton-Schulz chain of the batch before */
                                 /* it (side stream)                            */
 #define MA_PROF_NS_Q1 8         /* Gram-space chain: Q_1 = a I + b A_0         */
-#define MA_PROF_CLASSES 9
+#define MA_PROF_CLIP 9          /* global gradient norm, in-place clipping      */
+#define MA_PROF_CLASSES 10
 
 /* When on != 0, every kernel the library launches on this thread's current
  * device is bracketed by two CUDA events recorded on its launch stream. Off by
