@@ -24,7 +24,8 @@ __all__ = [
     "ma_set_wait_limit_ns", "ma_set_momentum_overlap", "ma_debug_build", "MA_ERR_BOUNDS",
     "ma_selftest_wait_timeout", "ma_profile_enable", "ma_profile_collect", "PROF_CLASSES", "group_table", "Plan",
     "MuonAdamW", "muon_hparams", "adamw_hparams", "CLIP_BYTES", "clip_buffer", "ma_grad_norm", "ma_grad_clip",
-    "ma_clip_finalize", "ma_plan_set_clip", "GradClip",
+    "ma_clip_finalize", "ma_plan_set_clip", "GradClip", "MA_I32", "MA_I64", "embedding_lookup",
+    "embed_grad_workspace_bytes", "embedding_grad", "embedding",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -35,7 +36,7 @@ LIB_PATH = os.path.join(HERE, "lib", "libmuonadamw_debug.so" if os.environ.get("
 
 MA_OK, MA_ERR_NULL, MA_ERR_SHAPE, MA_ERR_DTYPE, MA_ERR_ALIGN, MA_ERR_WORKSPACE = 0, 1, 2, 3, 4, 5
 MA_ERR_UNSUPPORTED, MA_ERR_CUDA, MA_ERR_TIMEOUT, MA_ERR_ARG, MA_ERR_BOUNDS = 6, 7, 8, 9, 10
-MA_F32, MA_BF16 = 0, 1
+MA_F32, MA_BF16, MA_I32, MA_I64 = 0, 1, 2, 3
 MA_MUON, MA_ADAMW = 0, 1
 ROLE_HIDDEN, ROLE_EMBED, ROLE_UNEMBED, ROLE_FORCE_ADAMW = 0, 1, 2, 3
 MAX_NS_STEPS = 16
@@ -135,6 +136,10 @@ def lib() -> ctypes.CDLL:
                                            ctypes.POINTER(AdamWHParams), vp, vp]),
         "muon_step_batched_clipped": (i32, [i32, i64, i64, pp, pp, i32, pp, ctypes.POINTER(MuonHParams), vp, vp, sz,
                                             vp]),
+        "ma_embed_lookup": (i32, [i64, vp, i32, i64, i64, vp, i32, i64, ctypes.c_float, i64, vp, i32, i64, vp]),
+        "ma_embed_grad_workspace_bytes": (sz, [i64, i64, i64]),
+        "ma_embed_grad": (i32, [i64, vp, i32, i64, i64, vp, i32, i64, ctypes.c_float, i64, i32, vp, i32, i64, vp, sz,
+                                vp]),
         "ma_plan_set_clip": (i32, [vp, i32, ctypes.c_float, ctypes.c_float, vp]),
         "adamw_step_fused": (i32, [i32, pp, pp, i32, pp, pp, ctypes.POINTER(ctypes.c_int64),
                                    ctypes.POINTER(AdamWHParams), vp]),
@@ -418,6 +423,148 @@ def ma_plan_set_clip(plan, clip, max_norm: float = math.inf, scale: float = 1.0,
            "ma_plan_set_clip")
 
 
+NO_PADDING = -(1 << 63)
+
+
+def _ids(ids, stream):
+    """Contiguous token ids and their dtype code."""
+    import torch
+    if ids.dtype not in (torch.int32, torch.int64):
+        raise MAError(MA_ERR_DTYPE, f"token ids must be int32 or int64, not {ids.dtype}")
+    if not ids.is_contiguous():
+        with _on_stream(stream):
+            ids = ids.contiguous()
+    return ids, (MA_I64 if ids.dtype == torch.int64 else MA_I32)
+
+
+def _rows(t, what: str):
+    """(tensor as rows x dim, row stride): the last dimension contiguous, the others evenly strided."""
+    if t.dim() != 2:
+        try:
+            t = t.view(math.prod(t.shape[:-1]), t.shape[-1])
+        except RuntimeError as e:
+            raise MAError(MA_ERR_SHAPE, f"{what}: rows are not evenly strided") from e
+    rows, dim = t.shape
+    if dim > 1 and t.stride(1) != 1:
+        raise MAError(MA_ERR_SHAPE, f"{what}: rows must be contiguous")
+    return t, (int(t.stride(0)) if rows > 1 else max(1, int(dim)))
+
+
+def _on_stream(stream):
+    """A context in which torch allocates for ``stream`` (None: the current one)."""
+    import contextlib
+
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream))
+    return torch.cuda.stream(s)
+
+
+def embedding_lookup(ids, table, scale: float = 1.0, padding: int | None = None, out=None, dtype=None, stream=None):
+    """Rows of an embedding table by token: out[...] = scale * table[ids[...]], rounded once to ``dtype`` (fp32 or
+    bf16; default: the table's), or into ``out`` (shape ids.shape + (dim,)). An id outside the table gives zeros and
+    records MA_ERR_BOUNDS in the status word, except ``padding`` (-1, say), which only gives zeros."""
+    import torch
+    _on_current_gpu("embedding_lookup", ids, table, out)
+    ids, idt = _ids(ids, stream)
+    if table.dim() != 2:
+        raise MAError(MA_ERR_SHAPE, "embedding_lookup: the table must be 2-D")
+    V, D = (int(s) for s in table.shape)
+    tab, ldt = _rows(table, "embedding_lookup: table")
+    if out is None:
+        with _on_stream(stream):
+            out = torch.empty(ids.shape + (D,), dtype=dtype or table.dtype, device=table.device)
+    elif out.shape != ids.shape + (D,) or (dtype is not None and out.dtype != dtype):
+        raise MAError(MA_ERR_SHAPE, "embedding_lookup: out has another shape or dtype")
+    rows, ldo = _rows(out, "embedding_lookup: out")
+    _check(lib().ma_embed_lookup(ids.numel(), _ptr(ids), idt, V, D, _ptr(tab), _dtype_code(table), ldt, float(scale),
+                                 NO_PADDING if padding is None else int(padding), _ptr(rows), _dtype_code(out), ldo,
+                                 _stream(stream)), "embedding_lookup")
+    return out
+
+
+def embed_grad_workspace_bytes(n: int, rows: int, dim: int) -> int:
+    """Workspace bytes embedding_grad needs for n tokens and a rows x dim table."""
+    v = lib().ma_embed_grad_workspace_bytes(int(n), int(rows), int(dim))
+    if v == ctypes.c_size_t(-1).value:
+        raise MAError(MA_ERR_ARG, "embed_grad_workspace_bytes")
+    return int(v)
+
+
+def embedding_grad(ids, grad_rows, grad, scale: float = 1.0, padding: int | None = None, accumulate: bool = False,
+                   ws=None, stream=None):
+    """Gradient of a table from those of the rows looked up, by sorted tokens: grad[v] = scale * sum of grad_rows
+    over the tokens that are v. Every row of ``grad`` (fp32 or bf16, the table's shape: the buffer the optimizer
+    reads) is written, zeros where no token points; with ``accumulate`` the sums are added to the rows that have
+    tokens. fp32 sums in token order, no atomics: the same inputs give the same bits. Tokens equal to ``padding``
+    add nothing. ws: workspace (embed_grad_workspace_bytes; allocated here when None). Returns ``grad``."""
+    import torch
+    _on_current_gpu("embedding_grad", ids, grad_rows, grad, ws)
+    ids, idt = _ids(ids, stream)
+    if grad.dim() != 2 or grad_rows.shape != ids.shape + (grad.shape[1],):
+        raise MAError(MA_ERR_SHAPE, "embedding_grad: grad must be rows x dim, grad_rows ids.shape + (dim,)")
+    V, D = (int(s) for s in grad.shape)
+    g, ldg = _rows(grad, "embedding_grad: grad")
+    y, ldy = _rows(grad_rows, "embedding_grad: grad_rows")
+    need = embed_grad_workspace_bytes(ids.numel(), V, D)
+    if ws is None and need:
+        with _on_stream(stream):
+            ws = torch.empty(need, dtype=torch.uint8, device=grad.device)
+    _check(lib().ma_embed_grad(ids.numel(), _ptr(ids), idt, V, D, _ptr(y), _dtype_code(grad_rows), ldy, float(scale),
+                               NO_PADDING if padding is None else int(padding), int(bool(accumulate)), _ptr(g),
+                               _dtype_code(grad), ldg, _ptr(ws),
+                               ws.numel() * ws.element_size() if ws is not None else 0, _stream(stream)),
+           "embedding_grad")
+    return grad
+
+
+_EMBEDDING = None
+
+
+def _embedding_function():
+    """The autograd function behind :func:`embedding` (made on first use: torch is imported lazily)."""
+    global _EMBEDDING
+    if _EMBEDDING is not None:
+        return _EMBEDDING
+    import torch
+    from torch.autograd.function import once_differentiable
+
+    class Embedding(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, ids, table, scale, padding, dtype, grad):
+            ctx.save_for_backward(ids)
+            ctx.args = scale, padding, grad, table.shape, table.dtype, table.device
+            return embedding_lookup(ids, table, scale, padding, dtype=dtype)
+
+        @staticmethod
+        @once_differentiable
+        def backward(ctx, dy):
+            (ids,) = ctx.saved_tensors
+            scale, padding, grad, shape, dtype, device = ctx.args
+            dy = dy.contiguous()
+            if grad is not None:
+                embedding_grad(ids, dy, grad, scale, padding, accumulate=True)
+                return (None,) * 6
+            out = torch.empty(shape, dtype=dtype, device=device)
+            return None, embedding_grad(ids, dy, out, scale, padding), None, None, None, None
+
+    _EMBEDDING = Embedding
+    return Embedding
+
+
+def embedding(ids, table, scale: float = 1.0, padding: int | None = None, dtype=None, grad=None):
+    """embedding_lookup with a gradient for the table (embedding_grad; not differentiable twice).
+
+    ``grad``: a fp32 or bf16 buffer of the table's shape that backward adds the
+    gradient to, in place of returning one: the buffer the optimizer reads can
+    then be filled over several micro-batches, and no table-sized gradient is
+    made and added. The caller zeroes it, and it is complete when backward is."""
+    if grad is not None and (tuple(grad.shape) != tuple(table.shape)):
+        raise MAError(MA_ERR_SHAPE, "embedding: grad must have the table's shape")
+    return _embedding_function().apply(ids, table, float(scale), padding, dtype, grad)
+
+
 def ma_plan_create(tensors: Sequence[Tensor], groups: Sequence[Group], ws_cap: int = 0):
     """Plan a parameter table; returns (plan handle, workspace bytes the step needs)."""
     n = len(tensors)
@@ -506,7 +653,7 @@ def ma_selftest_wait_timeout(limit_ns: int, stream=None) -> None:
 
 
 PROF_CLASSES = ("adamw", "momentum", "finalize", "ns_gram", "ns_apply", "ns_gramsq", "ns_final", "momentum_side",
-                "ns_q1", "clip")
+                "ns_q1", "clip", "embed")
 
 
 def ma_profile_enable(on: bool) -> None:

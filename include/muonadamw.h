@@ -53,11 +53,12 @@ typedef enum {
     MA_ERR_CUDA = 7,        /* a CUDA runtime call failed                         */
     MA_ERR_TIMEOUT = 8,     /* a device-side bounded wait ran out (status word)   */
     MA_ERR_ARG = 9,         /* a hyperparameter is out of its domain              */
-    MA_ERR_BOUNDS = 10      /* debug builds: a guarded device index fell outside  */
-                            /* its buffer and the access was skipped (status word) */
+    MA_ERR_BOUNDS = 10      /* a token id outside the embedding table; in debug   */
+                            /* builds also a guarded device index outside its     */
+                            /* buffer, the access skipped (status word)           */
 } ma_status_t;
 
-typedef enum { MA_F32 = 0, MA_BF16 = 1 } ma_dtype_t;
+typedef enum { MA_F32 = 0, MA_BF16 = 1, MA_I32 = 2, MA_I64 = 3 } ma_dtype_t; /* integers: token ids only */
 typedef enum { MA_MUON = 0, MA_ADAMW = 1 } ma_kind_t;
 
 /* Role of a tensor in the model. Muon is meant for hidden matrices whose input
@@ -337,6 +338,39 @@ int muon_step_batched_clipped(int batch, int64_t R, int64_t C, float* const* W, 
                               int gdt, float* const* M, const ma_muon_hparams_t* hp, const void* clip,
                               void* ws, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------- embedding */
+
+/* Rows of an embedding table by token, and the table's gradient by sorted
+ * tokens. The table is one of the step's tensors (MA_ROLE_EMBED), and its
+ * gradient is written where the step reads it.
+ *     out[i]  = scale * table[ids[i]]
+ *     grad[v] = scale * sum over {i : ids[i] = v} of dY[i]   (+ grad[v])
+ *  n: tokens. ids: device, MA_I32 or MA_I64 (idt). rows x dim: the table's
+ *     shape. ldt, ldo, ldy, ldg: row strides in elements, >= dim. Tables,
+ *     outputs and gradients are fp32 or bf16 each, any element alignment (rows
+ *     that begin at multiples of 16 bytes are fastest).
+ *  padding: an id whose tokens add nothing to the gradient (INT64_MIN: none).
+ *     The lookup returns its row like any other when it is one of the table's,
+ *     else (-1, say) zeros.
+ * Any other id outside the table reads zeros, adds nothing, and records
+ * MA_ERR_BOUNDS in the status word. Sums are fp32, each run of equal tokens in
+ * token order, rounded once; no atomics touch a value, so the same inputs give
+ * the same bits. accumulate 0 writes every row of grad, zeros where no token
+ * points; 1 adds to the rows that have tokens and leaves the others alone.
+ * Elements between dim and the row stride are left alone. Limits: n < 2^31,
+ * rows and dim up to 2^30, row strides up to 2^31 (MA_ERR_UNSUPPORTED). Outputs and workspace must not
+ * overlap each other or an input (MA_ERR_ARG).
+ *  ws: device workspace of ws_bytes >= ma_embed_grad_workspace_bytes(n, rows,
+ *     dim), 256-byte aligned, contents scratch; calls that overlap on the GPU
+ *     need one each. */
+int ma_embed_lookup(int64_t n, const void* ids, int idt, int64_t rows, int64_t dim, const void* table,
+                    int tdt, int64_t ldt, float scale, int64_t padding, void* out, int odt, int64_t ldo,
+                    void* stream);
+size_t ma_embed_grad_workspace_bytes(int64_t n, int64_t rows, int64_t dim);
+int ma_embed_grad(int64_t n, const void* ids, int idt, int64_t rows, int64_t dim, const void* dY, int ydt,
+                  int64_t ldy, float scale, int64_t padding, int accumulate, void* grad, int gdt,
+                  int64_t ldg, void* ws, size_t ws_bytes, void* stream);
+
 /* ---------------------------------------------------------------- whole step */
 
 /* Build a plan for a parameter table [P1 "The MuonAdamW Class Architecture"]:
@@ -436,7 +470,8 @@ void ma_plan_destroy(ma_plan_t* plan);
                                 /* it (side stream)                            */
 #define MA_PROF_NS_Q1 8         /* Gram-space chain: Q_1 = a I + b A_0         */
 #define MA_PROF_CLIP 9          /* global gradient norm, in-place clipping      */
-#define MA_PROF_CLASSES 10
+#define MA_PROF_EMBED 10        /* embedding lookup and gradient (all launches of a call) */
+#define MA_PROF_CLASSES 11
 
 /* When on != 0, every kernel the library launches on this thread's current
  * device is bracketed by two CUDA events recorded on its launch stream. Off by
