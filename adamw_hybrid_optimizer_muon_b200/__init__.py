@@ -25,7 +25,7 @@ __all__ = [
     "ma_selftest_wait_timeout", "ma_profile_enable", "ma_profile_collect", "PROF_CLASSES", "group_table", "Plan",
     "MuonAdamW", "muon_hparams", "adamw_hparams", "CLIP_BYTES", "clip_buffer", "ma_grad_norm", "ma_grad_clip",
     "ma_clip_finalize", "ma_plan_set_clip", "GradClip", "MA_I32", "MA_I64", "embedding_lookup",
-    "embed_grad_workspace_bytes", "embedding_grad", "embedding",
+    "embed_grad_workspace_bytes", "embedding_grad", "embedding", "qk_max_logit", "qk_clip",
 ]
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -140,6 +140,9 @@ def lib() -> ctypes.CDLL:
         "ma_embed_grad_workspace_bytes": (sz, [i64, i64, i64]),
         "ma_embed_grad": (i32, [i64, vp, i32, i64, i64, vp, i32, i64, ctypes.c_float, i64, i32, vp, i32, i64, vp, sz,
                                 vp]),
+        "ma_qk_max_logit": (i32, [i64, i64, i64, i32, i32, i32, vp, i64, i64, i64, vp, i64, i64, i64, vp, ctypes.c_float,
+                                  i32, i32, i32, vp, vp]),
+        "ma_qk_clip": (i32, [i32, i32, i64, i64, i64, vp, vp, vp, ctypes.c_float, ctypes.c_float, vp]),
         "ma_plan_set_clip": (i32, [vp, i32, ctypes.c_float, ctypes.c_float, vp]),
         "adamw_step_fused": (i32, [i32, pp, pp, i32, pp, pp, ctypes.POINTER(ctypes.c_int64),
                                    ctypes.POINTER(AdamWHParams), vp]),
@@ -565,6 +568,72 @@ def embedding(ids, table, scale: float = 1.0, padding: int | None = None, dtype=
     return _embedding_function().apply(ids, table, float(scale), padding, dtype, grad)
 
 
+def qk_max_logit(q, k, scale: float | None = None, causal: bool = True, offsets=None, max_len: int | None = None,
+                 absolute: bool = False, out=None, accumulate: bool = False, stream=None):
+    """Largest attention logit of each query head: max over sequences and visible pairs of scale * q_i . k_j (with
+    ``absolute``, of its magnitude), as ``heads`` floats on the device.
+
+    q: bf16, sequences x tokens x heads x dim, or tokens x heads x dim with
+    ``offsets`` (int32 on the device, sequences + 1 positions of sequences laid
+    end to end, none longer than ``max_len``; default: all tokens). k: the same
+    with a number of heads that divides q's. dim: a multiple of 8 up to 256;
+    strides multiples of 8. scale: default dim ** -0.5. ``accumulate`` takes the
+    maximum with what ``out`` holds. Without a visible pair: -inf; a NaN logit: NaN."""
+    import torch
+    _on_current_gpu("qk_max_logit", q, k, offsets, out)
+    nd = 3 if offsets is not None else 4
+    if q.dim() != nd or k.dim() != nd or q.shape[:-2] != k.shape[:-2] or q.shape[-1] != k.shape[-1]:
+        raise MAError(MA_ERR_SHAPE, "qk_max_logit: q and k must be (sequences x) tokens x heads x dim")
+    if q.dtype != torch.bfloat16 or k.dtype != torch.bfloat16:
+        raise MAError(MA_ERR_DTYPE, "qk_max_logit: q and k must be bf16")
+    H, KV, D = int(q.shape[-2]), int(k.shape[-2]), int(q.shape[-1])
+    if q.numel() and (q.stride(-1) != 1 or k.stride(-1) != 1):
+        raise MAError(MA_ERR_SHAPE, "qk_max_logit: dim must be contiguous")
+    if accumulate and out is None:
+        raise MAError(MA_ERR_NULL, "qk_max_logit: accumulate needs out")
+    if out is None:
+        with _on_stream(stream):
+            out = torch.empty(H, dtype=torch.float32, device=q.device)
+    elif out.shape != (H,) or out.dtype != torch.float32 or not out.is_contiguous():
+        raise MAError(MA_ERR_SHAPE, "qk_max_logit: out must be heads contiguous fp32 values")
+    if offsets is not None:
+        if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 1 or not offsets.is_contiguous():
+            raise MAError(MA_ERR_SHAPE, "qk_max_logit: offsets must be sequences + 1 contiguous int32 positions")
+        S, total = offsets.numel() - 1, int(q.shape[0])
+        T, qs, ks = total if max_len is None else int(max_len), 0, 0
+    else:
+        S, T, total = int(q.shape[0]), int(q.shape[1]), 0
+        qs, ks = int(q.stride(0)), int(k.stride(0))
+    _check(lib().ma_qk_max_logit(S, T, total, H, KV, D, _ptr(q), qs, int(q.stride(-3)), int(q.stride(-2)), _ptr(k), ks,
+                                 int(k.stride(-3)), int(k.stride(-2)), _ptr(offsets),
+                                 D ** -0.5 if scale is None else float(scale), int(bool(causal)), int(bool(absolute)),
+                                 int(bool(accumulate)), _ptr(out), _stream(stream)), "qk_max_logit")
+    return out
+
+
+def qk_clip(wq, wk, max_logit, tau: float = 100.0, alpha: float = 0.5, kv_heads: int | None = None, stream=None) -> None:
+    """QK-Clip of the query and key weights, in place: heads whose largest logit (``max_logit``, one fp32 value per
+    query head, as qk_max_logit gives it) exceeds ``tau`` are scaled so that it becomes tau. wq: (heads * q_rows) x
+    cols, wk: (kv_heads * k_rows) x cols, fp32, contiguous (kv_heads: default heads). The query weights take the
+    factor to the power alpha, the key weights the rest; a key head shared by several query heads takes what the
+    one furthest over needs, and its query heads' weights make up for it, so that each head's logits scale by its
+    own factor. Heads within tau, or whose maximum is not finite, are not touched."""
+    import torch
+    _on_current_gpu("qk_clip", wq, wk, max_logit)
+    for t in (wq, wk, max_logit):
+        if t.dtype != torch.float32:
+            raise MAError(MA_ERR_DTYPE, "qk_clip: weights and maxima must be fp32")
+        if not t.is_contiguous():
+            raise MAError(MA_ERR_SHAPE, "qk_clip: weights and maxima must be contiguous")
+    H = max_logit.numel()
+    KV = H if kv_heads is None else int(kv_heads)
+    if wq.dim() != 2 or wk.dim() != 2 or wq.shape[1] != wk.shape[1] or H < 1 or KV < 1 or wq.shape[0] % H or \
+            wk.shape[0] % KV:
+        raise MAError(MA_ERR_SHAPE, "qk_clip: weights must be (heads * rows) x cols")
+    _check(lib().ma_qk_clip(H, KV, int(wq.shape[0]) // H, int(wk.shape[0]) // KV, int(wq.shape[1]), _ptr(wq), _ptr(wk),
+                            _ptr(max_logit), float(tau), float(alpha), _stream(stream)), "qk_clip")
+
+
 def ma_plan_create(tensors: Sequence[Tensor], groups: Sequence[Group], ws_cap: int = 0):
     """Plan a parameter table; returns (plan handle, workspace bytes the step needs)."""
     n = len(tensors)
@@ -653,7 +722,7 @@ def ma_selftest_wait_timeout(limit_ns: int, stream=None) -> None:
 
 
 PROF_CLASSES = ("adamw", "momentum", "finalize", "ns_gram", "ns_apply", "ns_gramsq", "ns_final", "momentum_side",
-                "ns_q1", "clip", "embed")
+                "ns_q1", "clip", "embed", "qk")
 
 
 def ma_profile_enable(on: bool) -> None:

@@ -1,0 +1,832 @@
+// QK-Clip: each attention head's largest logit, and the query and key weights
+// scaled down by it ("MuonClip Optimizer", QK-Clip: scale Q and K when the
+// largest logit exceeds a threshold).
+//
+//   S_h   = max over sequences and visible (i, j) of scale * q_i . k_j   (or |.|)
+//   g_h   = min(1, tau / S_h)
+//   W_k of key head c   <- W_k * G_c^(1 - alpha),  G_c = min of g_h over its query heads
+//   W_q of query head h <- W_q * g_h / G_c^(1 - alpha)        (alike W_q g_h^alpha without shared heads)
+// so that every head's logits scale by its own g_h.
+//
+// The maximum is one GEMM per head without an output: bound by the tensor cores.
+// It runs as tcgen05.mma (bf16 operands, fp32 accumulators in TMEM); the
+// epilogue reads each accumulator once and keeps one running maximum per row.
+//
+// One CTA per SM, 320 threads: warp 0 loads (TMA), warp 1 issues the MMAs, two
+// groups of four warps reduce. A CTA holds 256 queries of one head, as two
+// blocks of 128 rows, in shared memory, and streams tiles of N keys past them,
+// 64 columns of the head dimension a stage; both blocks multiply a key tile
+// before it is released, which halves the key traffic from L2, and while one
+// block's accumulator is reduced the other's is computed.
+//
+// Work is counted in (128 queries x N keys) products, of which causality and the
+// sequences' ends leave only those with a visible pair. A maximum can be cut
+// anywhere, so the CTAs take equal shares of that count, wherever it falls in a
+// head or a sequence, with no scheduler and no second pass: each segment ends
+// in one atomic maximum per warp (order does not change a maximum).
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstring>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace ma {
+
+namespace {
+
+constexpr int kBK = 64;                       // columns of the head dimension per stage (128 bytes: the swizzle width)
+constexpr int kRows = 128;                    // queries per block of rows (TMEM lanes)
+constexpr int kThreads = 320;
+constexpr uint32_t kQChunk = kRows * kBK * 2;  // 16 KB
+constexpr uint32_t kSmemMax = 232448;          // 227 KB
+constexpr uint32_t kCtlBytes = 512;
+constexpr int kMaxChunks = 4;                  // head dimension up to 256
+constexpr int kMaxStages = 12;
+constexpr uint32_t kSleepNs = 20000;
+constexpr long long kDrainNs = 50000000LL;  // bound of the waits for this CTA's own copies and MMAs at its end
+
+struct QkLaunch {
+    CUtensorMap mq, mk;      // {dim, tokens, heads, sequences}
+    const int32_t* offsets;  // packed: first token of each sequence and the end; NULL: sequences of `len` tokens
+    int32_t seqs, len, total;  // len: tokens per sequence (packed: the longest); total: tokens of a packed batch
+    int32_t heads, kv, chunks, stages;
+    float scale;
+    float* out;
+    long long wait_limit_ns;
+    int* status;
+};
+
+struct QkCtl {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t q_full[2], q_empty[2];
+    uint64_t acc_full[4], acc_empty[4];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int32_t abort_flag;
+    int64_t units_begin, units_end;  // this CTA's share
+    int32_t b0;                      // the sequence it begins in
+    int32_t pad;
+    int64_t rest0;                   // units before it in that sequence
+};
+static_assert(sizeof(QkCtl) <= kCtlBytes, "control block");
+
+// Sequence b: first token, and length, both kept inside the batch whatever the
+// offsets hold (those that do not fit are recorded).
+struct Seq {
+    int32_t tok0, len;
+};
+__device__ __forceinline__ Seq sequence(const QkLaunch& L, int b) {
+    if (!L.offsets) return {0, L.len};
+    const int lo = L.offsets[b], hi = L.offsets[b + 1];
+    const int a = min(max(lo, 0), L.total);
+    const int n = min(max(min(hi, L.total) - a, 0), L.len);
+    if (a != lo || a + n != hi) record_error(L.status, MA_ERR_BOUNDS);
+    return {a, n};
+}
+
+// Units (a block of 128 queries times a tile of N keys) of one head of a
+// sequence of len tokens, before query block t (causal: block t sees the keys
+// up to its last query; ceil((t + 1) * 128 / N) tiles).
+template <int N, bool CAUSAL>
+__device__ __forceinline__ int64_t units_before(int64_t t, int len) {
+    if (!CAUSAL) return t * ((len + N - 1) / N);
+    return N == 256 ? (t + 1) * (t + 1) / 4 : t * (t + 1) / 2;
+}
+template <int N, bool CAUSAL>
+__device__ __forceinline__ int64_t units_of_head(int len) {
+    return units_before<N, CAUSAL>((len + kRows - 1) / kRows, len);
+}
+
+// A part of one item (256 queries of a head): units [u0, u1) of it, in the order
+// key tile by key tile, the lower block of rows first.
+struct Segment {
+    int b, h, q0, tok0, len;
+    int n0, n1;          // rows of the two blocks
+    int tiles0, tiles1;  // key tiles each of them sees
+    int u0, u1;
+    __device__ __forceinline__ void unit(int u, int& j, int& s) const {
+        if (n1 == 0) {
+            j = u;
+            s = 0;
+        } else if (u < 2 * tiles0) {
+            j = u >> 1;
+            s = u & 1;
+        } else {
+            j = u - tiles0;
+            s = 1;
+        }
+    }
+    // whether unit u is the first (last) of this segment that uses its key tile
+    __device__ __forceinline__ bool first_of_tile(int u) const {
+        return u == u0 || n1 == 0 || u >= 2 * tiles0 || (u & 1) == 0;
+    }
+    __device__ __forceinline__ bool last_of_tile(int u) const {
+        return u + 1 == u1 || n1 == 0 || u >= 2 * tiles0 || (u & 1) == 1;
+    }
+    __device__ __forceinline__ int count(int s) const {  // units of block s in [u0, u1)
+        if (n1 == 0) return s == 0 ? u1 - u0 : 0;
+        auto zeros = [&](int u) { return min(u, 2 * tiles0) + 1 >> 1; };  // units of block 0 before u
+        const int z = zeros(u1) - zeros(u0);
+        return s == 0 ? z : u1 - u0 - z;
+    }
+};
+
+// Walks this CTA's share, segment by segment; every role makes the same walk.
+template <int N, bool CAUSAL>
+struct Walk {
+    const QkLaunch& L;
+    int64_t left, rest;  // units left; units of (b, h) before the next one
+    int b, h, q;         // next item
+    Seq sq;
+    int64_t item0;       // units of (b, h) before item q
+
+    __device__ Walk(const QkLaunch& l, const QkCtl* c) : L(l), left(c->units_end - c->units_begin), b(c->b0) {
+        if (left <= 0) return;
+        sq = sequence(L, b);
+        const int64_t per_head = units_of_head<N, CAUSAL>(sq.len);
+        h = (int)(c->rest0 / per_head);
+        rest = c->rest0 - (int64_t)h * per_head;
+        int lo = 0, hi = (sq.len - 1) / (2 * kRows);
+        while (lo < hi) {  // last item that begins at or before `rest`
+            const int mid = (lo + hi + 1) >> 1;
+            if (units_before<N, CAUSAL>(2 * mid, sq.len) <= rest) lo = mid;
+            else hi = mid - 1;
+        }
+        q = lo;
+        item0 = units_before<N, CAUSAL>(2 * q, sq.len);
+    }
+    __device__ bool next(Segment& g) {
+        if (left <= 0) return false;
+        while (sq.len == 0) {  // units are left, so a sequence with tokens follows
+            sq = sequence(L, ++b);
+        }
+        g.b = L.offsets ? 0 : b;
+        g.h = h;
+        g.q0 = q * 2 * kRows;
+        g.tok0 = sq.tok0;
+        g.len = sq.len;
+        g.n0 = min(kRows, sq.len - g.q0);
+        g.n1 = max(0, min(kRows, sq.len - g.q0 - kRows));
+        const int all = (sq.len + N - 1) / N;
+        g.tiles0 = CAUSAL ? (g.q0 + g.n0 + N - 1) / N : all;
+        g.tiles1 = g.n1 == 0 ? 0 : CAUSAL ? (g.q0 + kRows + g.n1 + N - 1) / N : all;
+        const int units = g.tiles0 + g.tiles1;
+        g.u0 = (int)(rest - item0);
+        g.u1 = (int)min((int64_t)units, g.u0 + left);
+        left -= g.u1 - g.u0;
+        // to the next item: the next 256 queries, the next head, the next sequence
+        ++q;
+        item0 += units;
+        rest = item0;
+        if (q * 2 * kRows >= sq.len) {
+            q = 0;
+            item0 = rest = 0;
+            if (++h == L.heads) {
+                h = 0;
+                ++b;
+                if (left > 0) sq = sequence(L, b);
+            }
+        }
+        return true;
+    }
+};
+
+// 4-D tiled load global -> shared, completing on `bar`.
+__device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
+                                            int c2, int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
+        "[%2];" ::"r"(smem_u32(smem_dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+
+// Each thread of the warp reads 32 consecutive fp32 columns of its TMEM lane;
+// tmem_wait_ld before the first use.
+__device__ __forceinline__ void tmem_ld32_async(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32; ++i) asm volatile("" : "+r"(r[i]));  // no use of r moves above the wait
+}
+
+// A NaN among the operands gives NaN: a NaN logit shows in the result.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+template <bool ABS>
+__device__ __forceinline__ void reduce32(const uint32_t (&r)[32], float (&m)[4]) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+        float a = __uint_as_float(r[i]), b = __uint_as_float(r[i + 1]);
+        if (ABS) {
+            a = fabsf(a);
+            b = fabsf(b);
+        }
+        m[(i >> 1) & 3] = max3_nan(m[(i >> 1) & 3], a, b);
+    }
+}
+
+// The same over the first `n` columns only (n may be <= 0).
+template <bool ABS>
+__device__ __forceinline__ void reduce32_masked(const uint32_t (&r)[32], int n, float (&m)[4]) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        float a = __uint_as_float(r[i]);
+        if (ABS) a = fabsf(a);
+        m[i & 3] = max_nan(m[i & 3], i < n ? a : -INFINITY);
+    }
+}
+
+// Floats in order as the bits that the integer maximum and minimum order;
+// works from an initial -infinity. A NaN (0x7fffffff) is above everything.
+__device__ __forceinline__ void atomic_max_float(float* p, float v) {
+    v += 0.f;  // -0 to +0
+    if (v < 0.f) atomicMin(reinterpret_cast<unsigned*>(p), __float_as_uint(v));
+    else atomicMax(reinterpret_cast<int*>(p), (int)(isnan(v) ? 0x7fffffffu : __float_as_uint(v)));
+}
+
+template <int N, bool CAUSAL>
+__device__ __forceinline__ int64_t units_of_seq(const QkLaunch& L, int b) {
+    return (int64_t)L.heads * units_of_head<N, CAUSAL>(sequence(L, b).len);
+}
+
+// This CTA's share of the units: begin, end, and the sequence it begins in.
+// Packed batches: thread t adds up a contiguous part of the sequences.
+template <int N, bool CAUSAL>
+__device__ void find_share(const QkLaunch& L, QkCtl* ctl, int64_t* sums) {
+    if (!L.offsets) {
+        if (threadIdx.x == 0) {
+            const int64_t per_seq = units_of_seq<N, CAUSAL>(L, 0), total = per_seq * L.seqs;
+            ctl->units_begin = total * blockIdx.x / gridDim.x;
+            ctl->units_end = total * (blockIdx.x + 1) / gridDim.x;
+            ctl->b0 = (int)(ctl->units_begin / per_seq);
+            ctl->rest0 = ctl->units_begin % per_seq;
+        }
+        __syncthreads();
+        return;
+    }
+    const int per = (L.seqs + kThreads - 1) / kThreads;
+    const int b0 = min(L.seqs, (int)threadIdx.x * per), b1 = min(L.seqs, b0 + per);
+    int64_t mine = 0;
+    for (int b = b0; b < b1; ++b) mine += units_of_seq<N, CAUSAL>(L, b);
+    sums[threadIdx.x] = mine;
+    __syncthreads();
+    int64_t before = 0, total = 0;
+    for (int t = 0; t < kThreads; ++t) {
+        const int64_t v = sums[t];
+        if (t < (int)threadIdx.x) before += v;
+        total += v;
+    }
+    const int64_t begin = total * blockIdx.x / gridDim.x, end = total * (blockIdx.x + 1) / gridDim.x;
+    if (threadIdx.x == 0) {
+        ctl->units_begin = begin;
+        ctl->units_end = end;
+        ctl->b0 = 0;
+        ctl->rest0 = 0;
+    }
+    __syncthreads();
+    if (begin < end && before <= begin && begin < before + mine) {
+        for (int b = b0; b < b1; ++b) {
+            const int64_t u = units_of_seq<N, CAUSAL>(L, b);
+            if (begin < before + u) {
+                ctl->b0 = b;
+                ctl->rest0 = begin - before;
+                break;
+            }
+            before += u;
+        }
+    }
+    __syncthreads();
+}
+
+template <int N, bool CAUSAL, bool ABS>
+__global__ void __launch_bounds__(kThreads, 1) qk_max_kernel(const __grid_constant__ QkLaunch L) {
+    griddep_launch_dependents();
+    constexpr uint32_t kStage = N * kBK * 2;
+    constexpr int NB = 512 / N / 2;  // accumulators per block of rows
+    extern __shared__ __align__(16) uint8_t raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) / 1024 * 1024);
+    const int chunks = L.chunks, nst = L.stages;
+    uint8_t* qbuf = smem;  // [block of rows][chunk]
+    uint8_t* ring = qbuf + 2 * chunks * kQChunk;
+    QkCtl* ctl = reinterpret_cast<QkCtl*>(ring + nst * kStage);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long limit = L.wait_limit_ns;
+    const AbortCtl ab{&ctl->abort_flag, 0u};
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < nst; ++s) {
+            mbar_init(&ctl->full[s], 1);
+            mbar_init(&ctl->empty[s], 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&ctl->q_full[s], 1);
+            mbar_init(&ctl->q_empty[s], 1);
+        }
+        for (int a = 0; a < 2 * NB; ++a) {
+            mbar_init(&ctl->acc_full[a], 1);
+            mbar_init(&ctl->acc_empty[a], 4);  // the four warps of a block of rows
+        }
+        mbar_init(&ctl->drain, 1);
+        ctl->abort_flag = 0;
+        fence_barrier_init();
+        prefetch_tensormap(&L.mq);
+        prefetch_tensormap(&L.mk);
+    }
+    if (warp == 1) {
+        tmem_alloc(&ctl->tmem_base, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = ctl->tmem_base;
+    griddep_wait();
+    find_share<N, CAUSAL>(L, ctl, reinterpret_cast<int64_t*>(qbuf));  // qbuf is free until the first load
+    fence_proxy_async_smem();
+    __syncthreads();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0, uses = 0;
+            uint32_t phase = 0;
+            int q_uses[2] = {0, 0};
+            bool ok = true;
+            Walk<N, CAUSAL> walk(L, ctl);
+            Segment g;
+            while (ok && walk.next(g)) {
+                const int kvh = g.h / (L.heads / L.kv);
+                auto load_q = [&](int s) {
+                    if (!mbar_wait_ctl(&ctl->q_empty[s], (q_uses[s] & 1u) ^ 1u, ab, limit, L.status)) return false;
+                    ++q_uses[s];
+                    mbar_arrive_expect_tx(&ctl->q_full[s], chunks * kQChunk);
+                    for (int c = 0; c < chunks; ++c)
+                        tma_load_4d(qbuf + (s * chunks + c) * kQChunk, &L.mq, &ctl->q_full[s], c * kBK,
+                                    g.tok0 + g.q0 + s * kRows, g.h, g.b);
+                    return true;
+                };
+                bool need_q[2] = {g.count(0) > 0, g.count(1) > 0};
+                for (int u = g.u0; u < g.u1 && ok; ++u) {
+                    int j, s;
+                    g.unit(u, j, s);
+                    if (need_q[s]) {  // in the order the MMAs use them
+                        need_q[s] = false;
+                        if (!(ok = load_q(s))) break;
+                    }
+                    if (!g.first_of_tile(u)) continue;
+                    for (int c = 0; c < chunks; ++c) {
+                        if (!mbar_wait_ctl(&ctl->empty[stage], phase ^ 1u, ab, limit, L.status)) {
+                            ok = false;
+                            break;
+                        }
+                        mbar_arrive_expect_tx(&ctl->full[stage], kStage);
+                        tma_load_4d(ring + stage * kStage, &L.mk, &ctl->full[stage], c * kBK, g.tok0 + j * N, kvh, g.b);
+                        ++uses;
+                        if (++stage == nst) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                }
+            }
+            // every copy of this CTA has landed before it exits (an abort leaves some unread)
+            for (int s = 0; s < nst; ++s) {
+                const int n = uses / nst + (s < uses % nst ? 1 : 0);  // uses of stage s
+                if (n > 0) mbar_wait_ctl(&ctl->full[s], (n - 1) & 1u, ab, kDrainNs, L.status, 0, false, true);
+            }
+            for (int s = 0; s < 2; ++s)
+                if (q_uses[s] > 0)
+                    mbar_wait_ctl(&ctl->q_full[s], (q_uses[s] - 1) & 1u, ab, kDrainNs, L.status, 0, false, true);
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            constexpr uint32_t IDESC = idesc_bf16_f32(kRows, N, 0);
+            int stage = 0;
+            uint32_t phase = 0;
+            int q_uses[2] = {0, 0}, acc_uses[2] = {0, 0};
+            bool ok = true;
+            Walk<N, CAUSAL> walk(L, ctl);
+            Segment g;
+            while (ok && walk.next(g)) {
+                int left[2] = {g.count(0), g.count(1)};
+                bool fresh[2] = {true, true};
+                for (int u = g.u0; u < g.u1 && ok; ++u) {
+                    int j, s;
+                    g.unit(u, j, s);
+                    const int a = s * NB + acc_uses[s] % NB;
+                    if (!mbar_wait_ctl(&ctl->acc_empty[a], ((acc_uses[s] / NB) & 1u) ^ 1u, ab, limit, L.status)) {
+                        ok = false;
+                        break;
+                    }
+                    if (fresh[s]) {
+                        fresh[s] = false;
+                        if (!mbar_wait_ctl(&ctl->q_full[s], q_uses[s] & 1u, ab, limit, L.status)) {
+                            ok = false;
+                            break;
+                        }
+                        ++q_uses[s];
+                    }
+                    tc_fence_after();
+                    const bool first = g.first_of_tile(u), last = g.last_of_tile(u);
+                    const uint32_t d = tmem + (uint32_t)(a * N);
+                    int st = stage;
+                    uint32_t ph = phase;
+                    for (int c = 0; c < chunks; ++c) {
+                        if (first) {
+                            if (!mbar_wait_ctl(&ctl->full[st], ph, ab, limit, L.status)) {
+                                ok = false;
+                                break;
+                            }
+                            tc_fence_after();
+                        }
+                        const uint32_t a0 = smem_u32(qbuf + (s * chunks + c) * kQChunk);
+                        const uint32_t b0 = smem_u32(ring + st * kStage);
+#pragma unroll
+                        for (int kk = 0; kk < kBK / 16; ++kk)
+                            tc_mma_f16(d, smem_desc_sw128(a0 + kk * 32, 16, 1024), smem_desc_sw128(b0 + kk * 32, 16, 1024),
+                                       IDESC, (c | kk) != 0 ? 1u : 0u);
+                        if (last) tc_commit(&ctl->empty[st]);
+                        if (++st == nst) {
+                            st = 0;
+                            ph ^= 1u;
+                        }
+                    }
+                    if (!ok) break;
+                    if (last) {
+                        stage = st;
+                        phase = ph;
+                    }
+                    ++acc_uses[s];
+                    if (--left[s] == 0) tc_commit(&ctl->q_empty[s]);
+                    tc_commit(&ctl->acc_full[a]);
+                }
+            }
+            tc_commit(&ctl->drain);  // every MMA has read its operands before this CTA exits
+            mbar_wait_ctl(&ctl->drain, 0, ab, kDrainNs, L.status, 0, false, true);
+        }
+    } else {
+        const int quad = warp & 3, s = (warp - 2) >> 2;
+        const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
+        int uses = 0;
+        bool ok = true;
+        Walk<N, CAUSAL> walk(L, ctl);
+        Segment g;
+        while (ok && walk.next(g)) {
+            const int i = g.q0 + s * kRows + quad * 32 + lane;  // this thread's query
+            const int lim = i >= g.len ? -1 : CAUSAL ? i : g.len - 1;  // its last visible key
+            float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            bool any = false;
+            for (int u = g.u0; u < g.u1; ++u) {
+                int j, us;
+                g.unit(u, j, us);
+                if (us != s) continue;
+                any = true;
+                const int a = s * NB + uses % NB;
+                int got = 1;
+                if (lane == 0) got = mbar_wait_ctl(&ctl->acc_full[a], (uses / NB) & 1u, ab, limit, L.status, kSleepNs);
+                if (!__shfl_sync(0xffffffffu, got, 0)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t t0 = lane_base + (uint32_t)(a * N);
+                const int n = lim - j * N + 1;  // columns of this tile the query sees
+                uint32_t r0[32], r1[32];
+                if (__all_sync(0xffffffffu, n >= N)) {
+                    tmem_ld32_async(t0, r0);
+                    tmem_wait_ld(r0);
+#pragma unroll
+                    for (int c = 0; c < N / 32; c += 2) {
+                        tmem_ld32_async(t0 + (c + 1) * 32, r1);
+                        reduce32<ABS>(r0, m);
+                        tmem_wait_ld(r1);
+                        if (c + 2 < N / 32) tmem_ld32_async(t0 + (c + 2) * 32, r0);
+                        reduce32<ABS>(r1, m);
+                        if (c + 2 < N / 32) tmem_wait_ld(r0);
+                    }
+                } else {
+                    const int most = __reduce_max_sync(0xffffffffu, n);
+                    for (int c = 0; c * 32 < min(most, N); ++c) {
+                        tmem_ld32_async(t0 + c * 32, r0);
+                        tmem_wait_ld(r0);
+                        reduce32_masked<ABS>(r0, n - c * 32, m);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl->acc_empty[a]);
+                ++uses;
+            }
+            if (!ok || !any) continue;
+            float v = max_nan(max_nan(m[0], m[1]), max_nan(m[2], m[3]));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
+            if (lane == 0 && v != -INFINITY) atomic_max_float(&L.out[g.h], v * L.scale);
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+__global__ void __launch_bounds__(256) qk_init_kernel(float* out, int heads) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int h = blockIdx.x * 256 + threadIdx.x;
+    if (h < heads) out[h] = -INFINITY;
+}
+
+// ------------------------------------------------------------------ weights
+
+constexpr int kScaleThreads = 256;
+constexpr int64_t kScaleChunk = 8192;  // floats per piece of a head's rows
+constexpr int kMaxHeads = 2048;        // query and key heads together
+
+struct QkScale {
+    float *wq, *wk;
+    const float* top;  // largest logit per query head
+    int64_t nq, nk;    // weights per query head, per key head
+    int32_t heads, kv, vec;
+    float tau, alpha;
+    int* status;
+};
+
+// g = min(1, tau / S); a maximum that is not finite (or below -tau) leaves the weights alone
+__device__ __forceinline__ float gamma_of(float s, float tau) { return s > tau && s < INFINITY ? tau / s : 1.f; }
+__device__ __forceinline__ float share(float g, float e) { return g == 1.f ? 1.f : e == 0.5f ? sqrtf(g) : powf(g, e); }
+
+// Every block lists the heads whose factor is not 1, then takes its share of
+// their pieces. A head within the threshold costs nothing.
+__global__ void __launch_bounds__(kScaleThreads) qk_scale_kernel(const __grid_constant__ QkScale A) {
+    griddep_launch_dependents();
+    griddep_wait();
+    __shared__ float factor[kMaxHeads];
+    __shared__ int16_t list[kMaxHeads];
+    __shared__ int count[2];
+    const int group = A.heads / A.kv;
+    for (int c = threadIdx.x; c < A.kv; c += kScaleThreads) {
+        float least = 1.f;
+        for (int k = 0; k < group; ++k) least = fminf(least, gamma_of(A.top[c * group + k], A.tau));
+        const float fk = share(least, 1.f - A.alpha);
+        factor[A.heads + c] = fk;
+        for (int k = 0; k < group; ++k) {
+            const float g = gamma_of(A.top[c * group + k], A.tau);
+            // without shared heads this is g^alpha; formed as the quotient so that the two factors multiply to g
+            factor[c * group + k] = group == 1 ? share(g, A.alpha) : g / fk;
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        int n = 0;
+        for (int part = 0; part < 2; ++part) {  // query heads first, then key heads
+            const int h0 = part ? A.heads : 0, h1 = part ? A.heads + A.kv : A.heads;
+            for (int h = h0 + (int)threadIdx.x; h - (int)threadIdx.x < h1; h += 32) {
+                const bool on = h < h1 && factor[h] != 1.f;
+                const uint32_t b = __ballot_sync(0xffffffffu, on);
+                if (on) list[n + __popc(b & ((1u << threadIdx.x) - 1))] = (int16_t)h;
+                n += __popc(b);
+            }
+            if (threadIdx.x == 0) count[part] = n;
+        }
+    }
+    __syncthreads();
+    const int64_t pq = (A.nq + kScaleChunk - 1) / kScaleChunk, pk = (A.nk + kScaleChunk - 1) / kScaleChunk;
+    const int64_t nq = count[0] * pq, all = nq + (count[1] - count[0]) * pk;
+    for (int64_t p = blockIdx.x; p < all; p += gridDim.x) {
+        const bool isq = p < nq;
+        const int64_t per = isq ? pq : pk, o = isq ? p : p - nq, n = isq ? A.nq : A.nk;
+        const int h = list[(isq ? 0 : count[0]) + o / per];
+        const int64_t i0 = o % per * kScaleChunk, i1 = min(n, i0 + kScaleChunk);
+        float* w = isq ? A.wq + h * A.nq : A.wk + (h - A.heads) * A.nk;
+        [[maybe_unused]] const int64_t at = isq ? h * A.nq : (h - A.heads) * A.nk;
+        [[maybe_unused]] const int64_t end = isq ? A.heads * A.nq : A.kv * A.nk;
+        const float f = factor[h];
+        if (A.vec) {
+#pragma unroll 8
+            for (int64_t i = i0 + 4 * threadIdx.x; i < i1; i += 4 * kScaleThreads) {
+                if (!MA_INB(at + i, 4, end, A.status)) continue;
+                float4 x = *reinterpret_cast<const float4*>(w + i);
+                x.x *= f; x.y *= f; x.z *= f; x.w *= f;
+                *reinterpret_cast<float4*>(w + i) = x;
+            }
+        } else {
+            for (int64_t i = i0 + threadIdx.x; i < i1; i += kScaleThreads)
+                if (MA_INB(at + i, 1, end, A.status)) w[i] *= f;
+        }
+    }
+}
+
+// ------------------------------------------------------------------ host
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_fn() {
+    static const EncodeTiledFn fn = []() -> EncodeTiledFn {
+        void* ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            return reinterpret_cast<EncodeTiledFn>(ptr);
+        return nullptr;
+    }();
+    return fn;
+}
+
+bool make_map(CUtensorMap* map, const void* base, int64_t dim, int64_t tokens, int64_t heads, int64_t seqs, int64_t st,
+              int64_t sh, int64_t sb, int box_rows) {
+    EncodeTiledFn enc = encode_fn();
+    if (!enc) return false;
+    const cuuint64_t dims[4] = {(cuuint64_t)dim, (cuuint64_t)tokens, (cuuint64_t)heads, (cuuint64_t)seqs};
+    const cuuint64_t strides[3] = {(cuuint64_t)st * 2, (cuuint64_t)sh * 2, (cuuint64_t)sb * 2};
+    const cuuint32_t box[4] = {kBK, (cuuint32_t)box_rows, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int N, bool CAUSAL, bool ABS>
+cudaError_t launch_max(const QkLaunch& L, int grid, uint32_t smem, cudaStream_t s) {
+    static PerDevice<int> cache;
+    int dev = 0, done = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    e = cache.get(dev, &done, [](int* v) {
+        *v = 1;
+        return cudaFuncSetAttribute(qk_max_kernel<N, CAUSAL, ABS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)kSmemMax);
+    });
+    if (e != cudaSuccess) return e;
+    return launch_pdl(qk_max_kernel<N, CAUSAL, ABS>, dim3(grid), dim3(kThreads), smem, s, L);
+}
+
+template <int N>
+cudaError_t launch_max_n(const QkLaunch& L, bool causal, bool abs, int grid, uint32_t smem, cudaStream_t s) {
+    if (causal) return abs ? launch_max<N, true, true>(L, grid, smem, s) : launch_max<N, true, false>(L, grid, smem, s);
+    return abs ? launch_max<N, false, true>(L, grid, smem, s) : launch_max<N, false, false>(L, grid, smem, s);
+}
+
+// Keys per tile: 256, or 128 for head dimensions above 192, whose key tile of
+// 256 would not fit beside the queries.
+int tile_keys(int dim) { return dim > 192 ? 128 : 256; }
+
+}  // namespace
+}  // namespace ma
+
+using namespace ma;
+
+namespace {
+
+int qk_max(int64_t seqs, int64_t len, int64_t total, int heads, int kv_heads, int dim, const uint16_t* q, int64_t q_seq,
+           int64_t q_tok, int64_t q_head, const uint16_t* k, int64_t k_seq, int64_t k_tok, int64_t k_head,
+           const int32_t* offsets, float scale, int causal, int absolute, int accumulate, float* out, void* stream) {
+    if (seqs < 0 || len < 0 || total < 0 || heads < 1 || kv_heads < 1 || dim < 1 || heads % kv_heads != 0)
+        return MA_ERR_SHAPE;
+    if (dim > kMaxChunks * kBK || heads > 65535 || seqs > INT_MAX - 1 || len > (INT_MAX >> 1) || total > (INT_MAX >> 1))
+        return MA_ERR_UNSUPPORTED;
+    if (!(scale > 0.f) || !std::isfinite(scale)) return MA_ERR_ARG;
+    if ((causal | absolute | accumulate) & ~1) return MA_ERR_ARG;
+    if (!out) return MA_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(out) % 4 != 0 || reinterpret_cast<uintptr_t>(offsets) % 4 != 0) return MA_ERR_ALIGN;
+    const int64_t tokens = offsets ? total : len, outer = offsets ? 1 : seqs;
+    const bool work = seqs > 0 && len > 0 && tokens > 0;
+    if (work) {
+        if (!q || !k) return MA_ERR_NULL;
+        if (dim % 8 != 0 || reinterpret_cast<uintptr_t>(q) % 16 != 0 || reinterpret_cast<uintptr_t>(k) % 16 != 0)
+            return MA_ERR_ALIGN;
+        const int64_t st[6] = {q_tok, q_head, q_seq, k_tok, k_head, k_seq};
+        const int64_t ext[6] = {tokens, heads, outer, tokens, kv_heads, outer};
+        for (int i = 0; i < 6; ++i) {
+            if (st[i] < 0 || (ext[i] > 1 && st[i] < dim)) return MA_ERR_SHAPE;
+            if (st[i] % 8 != 0) return MA_ERR_ALIGN;
+            if (st[i] >= (int64_t(1) << 38)) return MA_ERR_UNSUPPORTED;
+        }
+    }
+    int sms = 0, st;
+    if ((st = device_ready(&sms))) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    QkLaunch L;
+    std::memset(&L, 0, sizeof(L));
+    const int n = tile_keys(dim);
+    L.chunks = (dim + kBK - 1) / kBK;
+    if (work) {
+        // a stride of an extent of 1 is never followed, but the map wants one of at least 16 bytes
+        auto fix = [&](int64_t x) { return x > 0 ? x : (int64_t)8 * ((dim + 7) / 8); };
+        if (!make_map(&L.mq, q, dim, tokens, heads, outer, fix(q_tok), fix(q_head), fix(q_seq), kRows) ||
+            !make_map(&L.mk, k, dim, tokens, kv_heads, outer, fix(k_tok), fix(k_head), fix(k_seq), n))
+            return MA_ERR_CUDA;
+    }
+    const int pr = prof_begin(MA_PROF_QK, s);
+    cudaError_t e = cudaSuccess;
+    if (!accumulate) e = launch_pdl(qk_init_kernel, dim3((heads + 255) / 256), dim3(256), 0, s, out, heads);
+    double flops = 0.0;
+    if (e == cudaSuccess && work) {
+        L.offsets = offsets;
+        L.seqs = (int)seqs;
+        L.len = (int)len;
+        L.total = (int)total;
+        L.heads = heads;
+        L.kv = kv_heads;
+        L.scale = scale;
+        L.out = out;
+        L.wait_limit_ns = host_wait_limit_ns();
+        L.status = device_status_ptr();
+        const uint32_t qbytes = 2 * L.chunks * kQChunk, stage = n * kBK * 2;
+        L.stages = std::min<int>(kMaxStages, (int)((kSmemMax - 1024 - kCtlBytes - qbytes) / stage));
+        const uint32_t smem = 1024 + qbytes + L.stages * stage + kCtlBytes;
+        // a CTA per SM; fewer when there are fewer units (dense batches: the host knows)
+        int grid = sms;
+        if (!offsets) {
+            const int64_t m = (len + kRows - 1) / kRows;
+            const int64_t units = (causal ? (n == 256 ? (m + 1) * (m + 1) / 4 : m * (m + 1) / 2) : m * ((len + n - 1) / n)) *
+                                  heads;
+            grid = (int)std::min<int64_t>(sms, units * std::min<int64_t>(seqs, sms));
+            flops = 2.0 * dim * heads * (double)seqs * (causal ? 0.5 * len * (len + 1.0) : (double)len * len);
+        }
+        e = n == 256 ? launch_max_n<256>(L, causal, absolute, grid, smem, s)
+                     : launch_max_n<128>(L, causal, absolute, grid, smem, s);
+    }
+    prof_end(pr, s, flops, 0.0);
+    return e == cudaSuccess ? MA_OK : MA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int ma_qk_max_logit(int64_t seqs, int64_t len, int64_t total, int heads, int kv_heads, int dim, const uint16_t* q,
+                    int64_t q_seq, int64_t q_tok, int64_t q_head, const uint16_t* k, int64_t k_seq, int64_t k_tok,
+                    int64_t k_head, const int32_t* offsets, float scale, int causal, int absolute, int accumulate,
+                    float* out, void* stream) {
+    return qk_max(seqs, len, total, heads, kv_heads, dim, q, q_seq, q_tok, q_head, k, k_seq, k_tok, k_head, offsets,
+                  scale, causal, absolute, accumulate, out, stream);
+}
+
+int ma_qk_clip(int heads, int kv_heads, int64_t q_rows, int64_t k_rows, int64_t cols, float* wq, float* wk,
+               const float* max_logit, float tau, float alpha, void* stream) {
+    if (heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || q_rows < 0 || k_rows < 0 || cols < 0) return MA_ERR_SHAPE;
+    if (heads + kv_heads > kMaxHeads || q_rows > (int64_t(1) << 30) || k_rows > (int64_t(1) << 30) ||
+        cols > (int64_t(1) << 30))
+        return MA_ERR_UNSUPPORTED;
+    if (!(tau > 0.f) || !std::isfinite(tau) || !(alpha >= 0.f && alpha <= 1.f)) return MA_ERR_ARG;
+    if (!max_logit) return MA_ERR_NULL;
+    QkScale A;
+    std::memset(&A, 0, sizeof(A));
+    A.nq = q_rows * cols;
+    A.nk = k_rows * cols;
+    if ((A.nq > 0 && !wq) || (A.nk > 0 && !wk)) return MA_ERR_NULL;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(wq), b = reinterpret_cast<uintptr_t>(wk),
+                    c = reinterpret_cast<uintptr_t>(max_logit);
+    if (a % 4 != 0 || b % 4 != 0 || c % 4 != 0) return MA_ERR_ALIGN;
+    const uintptr_t ab = (uintptr_t)A.nq * heads * 4, bb = (uintptr_t)A.nk * kv_heads * 4, cb = (uintptr_t)heads * 4;
+    auto meet = [](uintptr_t x, uintptr_t xb, uintptr_t y, uintptr_t yb) { return xb && yb && x < y + yb && y < x + xb; };
+    if (meet(a, ab, b, bb) || meet(a, ab, c, cb) || meet(b, bb, c, cb)) return MA_ERR_ARG;
+    int sms = 0, st;
+    if ((st = device_ready(&sms))) return st;
+    if (A.nq == 0 && A.nk == 0) return MA_OK;
+    A.wq = wq;
+    A.wk = wk;
+    A.top = max_logit;
+    A.heads = heads;
+    A.kv = kv_heads;
+    A.vec = a % 16 == 0 && b % 16 == 0 && A.nq % 4 == 0 && A.nk % 4 == 0;
+    A.tau = tau;
+    A.alpha = alpha;
+    A.status = device_status_ptr();
+    const int64_t pieces = heads * ((A.nq + kScaleChunk - 1) / kScaleChunk) + kv_heads * ((A.nk + kScaleChunk - 1) / kScaleChunk);
+    const int grid = (int)std::min<int64_t>(pieces, 4 * (int64_t)sms);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int pr = prof_begin(MA_PROF_QK, s);
+    const cudaError_t e = launch_pdl(qk_scale_kernel, dim3(grid), dim3(kScaleThreads), 0, s, A);
+    prof_end(pr, s, 0.0, 0.0);
+    return e == cudaSuccess ? MA_OK : MA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -371,6 +371,44 @@ int ma_embed_grad(int64_t n, const void* ids, int idt, int64_t rows, int64_t dim
                   int64_t ldy, float scale, int64_t padding, int accumulate, void* grad, int gdt,
                   int64_t ldg, void* ws, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------- QK-Clip */
+
+/* QK-Clip [P5 "MuonClip Optimizer": scale Q and K when the largest attention
+ * logit exceeds a threshold]: the largest logit of each query head over a
+ * batch, then the weights that made it, scaled down.
+ *     S_h = max over sequences and visible (i, j) of scale * q_i . k_j
+ * with absolute != 0 of its magnitude. Query head h reads key head
+ * h / (heads / kv_heads). causal: key j is visible to queries i >= j of its
+ * sequence, else all of its sequence's keys are. q, k: device, bf16 bit
+ * patterns, `heads` (`kv_heads`) vectors of dim <= 256 per token, dim % 8 == 0,
+ * 16-byte aligned, strides in elements and multiples of 8, no less than dim.
+ *  offsets NULL: seqs sequences of len tokens, at q_seq (k_seq) from each other.
+ *  offsets: device, seqs + 1 token positions; sequences lie end to end in
+ *     `total` tokens (q_seq and k_seq are not used) and none is longer than
+ *     len; they may be empty. Positions outside 0..total, out of order, or
+ *     more than len apart are cut to fit and record MA_ERR_BOUNDS in the status word.
+ *  out: device, `heads` floats. accumulate 0: set; 1: the maximum with what is
+ *     there (several calls make one batch). -infinity: no visible pair. A NaN
+ *     logit makes its head's maximum NaN.
+ * fp32 accumulation of the exact bf16 products; a maximum does not depend on
+ * the order, so the same inputs give the same bits. */
+int ma_qk_max_logit(int64_t seqs, int64_t len, int64_t total, int heads, int kv_heads, int dim,
+                    const uint16_t* q, int64_t q_seq, int64_t q_tok, int64_t q_head,
+                    const uint16_t* k, int64_t k_seq, int64_t k_tok, int64_t k_head,
+                    const int32_t* offsets, float scale, int causal, int absolute, int accumulate,
+                    float* out, void* stream);
+
+/* The weights, in place: with g_h = min(1, tau / S_h) (1 where S_h is not
+ * finite) and G_c the least g_h of the query heads of key head c,
+ *     rows of key head c   of W_k times G_c^(1 - alpha)
+ *     rows of query head h of W_q times g_h / G_c^(1 - alpha)
+ * so that head h's logits scale by g_h; W_q's factor is g_h^alpha where no key
+ * head is shared. wq: heads * q_rows x cols, wk: kv_heads * k_rows x cols,
+ * device, fp32, row-major, head after head. Rows whose factor is 1 are not
+ * touched. 0 <= alpha <= 1 (1/2: shared evenly). At most 2048 heads in all. */
+int ma_qk_clip(int heads, int kv_heads, int64_t q_rows, int64_t k_rows, int64_t cols, float* wq, float* wk,
+               const float* max_logit, float tau, float alpha, void* stream);
+
 /* ---------------------------------------------------------------- whole step */
 
 /* Build a plan for a parameter table [P1 "The MuonAdamW Class Architecture"]:
@@ -471,7 +509,8 @@ void ma_plan_destroy(ma_plan_t* plan);
 #define MA_PROF_NS_Q1 8         /* Gram-space chain: Q_1 = a I + b A_0         */
 #define MA_PROF_CLIP 9          /* global gradient norm, in-place clipping      */
 #define MA_PROF_EMBED 10        /* embedding lookup and gradient (all launches of a call) */
-#define MA_PROF_CLASSES 11
+#define MA_PROF_QK 11           /* QK-Clip: largest logits, weight scaling     */
+#define MA_PROF_CLASSES 12
 
 /* When on != 0, every kernel the library launches on this thread's current
  * device is bracketed by two CUDA events recorded on its launch stream. Off by
