@@ -8,6 +8,7 @@ the C names (``ma_partition``, ``muon_step_batched``, ``adamw_step_fused``,
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -127,10 +128,8 @@ def lib() -> ctypes.CDLL:
         "muon_step_batched": (i32, [i32, i64, i64, pp, pp, i32, pp, ctypes.POINTER(MuonHParams), vp, sz, vp]),
         "ns_iterate_workspace_bytes": (sz, [i32, i64, i64]),
         "ns_iterate_bf16": (i32, [i32, i64, i64, vp, vp, ctypes.POINTER(ctypes.c_float), i32, i32, vp, sz, vp]),
-        "ma_grad_norm": (i32, [i32, pp, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int64), ctypes.c_float,
-                               ctypes.c_float, vp, vp]),
-        "ma_grad_clip": (i32, [i32, pp, ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int64), ctypes.c_float,
-                               ctypes.c_float, vp, vp]),
+        "ma_grad_norm": (i32, [i32, vp, vp, vp, ctypes.c_float, ctypes.c_float, vp, vp]),
+        "ma_grad_clip": (i32, [i32, vp, vp, vp, ctypes.c_float, ctypes.c_float, vp, vp]),
         "ma_clip_finalize": (i32, [ctypes.c_float, ctypes.c_float, vp, vp]),
         "adamw_step_fused_clipped": (i32, [i32, pp, pp, i32, pp, pp, ctypes.POINTER(ctypes.c_int64),
                                            ctypes.POINTER(AdamWHParams), vp, vp]),
@@ -202,15 +201,30 @@ def _ptr(x) -> int:
 
 
 def _ptr_array(xs) -> ctypes.Array:
-    arr = (ctypes.c_void_p * max(1, len(xs)))()
-    for i, x in enumerate(xs):
-        arr[i] = _ptr(x)
-    return arr
+    try:
+        ptrs = [x.data_ptr() for x in xs]
+    except AttributeError:  # plain addresses, or None, among them
+        ptrs = [_ptr(x) for x in xs]
+    return (ctypes.c_void_p * max(1, len(ptrs)))(*ptrs)
+
+
+_TORCH = None
+
+
+def _torch():
+    """The torch module, imported on first use."""
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _stream(stream) -> int:
     if stream is None:
-        import torch
+        torch = _torch()
+        if torch.cuda.is_initialized():  # the handle itself, without a Stream object around it
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return int(torch.cuda.current_stream().cuda_stream)
     if isinstance(stream, int):
         return stream
@@ -218,12 +232,13 @@ def _stream(stream) -> int:
 
 
 def _dtype_code(t) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
+    torch = _torch()
+    dt = t.dtype
+    if dt is torch.bfloat16:
         return MA_BF16
-    if t.dtype == torch.float32:
+    if dt is torch.float32:
         return MA_F32
-    raise MAError(MA_ERR_DTYPE, f"unsupported gradient dtype {t.dtype}")
+    raise MAError(MA_ERR_DTYPE, f"unsupported gradient dtype {dt}")
 
 
 def muon_hparams(lr=0.02, beta=0.95, weight_decay=0.01, eps=1e-7, nesterov=True, ns_steps=5,
@@ -363,7 +378,7 @@ def adamw_step_fused(P, G, M, V, hp: AdamWHParams, stream=None, gdt: int | None 
     if gdt is None:
         gdt = _dtype_code(G[0]) if n else MA_F32
     if numel is None:
-        numel = [int(p.numel()) for p in P]
+        numel = [p.numel() for p in P]
     nar = (ctypes.c_int64 * max(1, n))(*numel)
     _check(lib().adamw_step_fused_clipped(n, _ptr_array(P), _ptr_array(G), int(gdt), _ptr_array(M), _ptr_array(V),
                                           nar, ctypes.byref(hp), _ptr(clip), _stream(stream)), "adamw_step_fused")
@@ -381,9 +396,13 @@ def clip_buffer(device=None):
 
 def _on_current_gpu(what: str, *tensors) -> None:
     """Refuse tensors that are not on the current CUDA device (the one the launch goes to)."""
-    import torch
+    current = None
     for t in tensors:
-        if t is not None and not (t.is_cuda and t.device.index == torch.cuda.current_device()):
+        if t is None:
+            continue
+        if current is None and t.is_cuda:
+            current = _torch()._C._cuda_getDevice()
+        if not t.is_cuda or t.get_device() != current:
             raise MAError(MA_ERR_ARG, f"{what}: tensor on {t.device}, not on the current CUDA device")
 
 
@@ -431,17 +450,23 @@ NO_PADDING = -(1 << 63)
 
 def _ids(ids, stream):
     """Contiguous token ids and their dtype code."""
-    import torch
-    if ids.dtype not in (torch.int32, torch.int64):
+    torch = _torch()
+    if ids.dtype is torch.int64:
+        idt = MA_I64
+    elif ids.dtype is torch.int32:
+        idt = MA_I32
+    else:
         raise MAError(MA_ERR_DTYPE, f"token ids must be int32 or int64, not {ids.dtype}")
     if not ids.is_contiguous():
         with _on_stream(stream):
             ids = ids.contiguous()
-    return ids, (MA_I64 if ids.dtype == torch.int64 else MA_I32)
+    return ids, idt
 
 
 def _rows(t, what: str):
     """(tensor as rows x dim, row stride): the last dimension contiguous, the others evenly strided."""
+    if t.is_contiguous():
+        return t, max(1, t.shape[-1])
     if t.dim() != 2:
         try:
             t = t.view(math.prod(t.shape[:-1]), t.shape[-1])
@@ -453,13 +478,14 @@ def _rows(t, what: str):
     return t, (int(t.stride(0)) if rows > 1 else max(1, int(dim)))
 
 
+_HERE = contextlib.nullcontext()
+
+
 def _on_stream(stream):
     """A context in which torch allocates for ``stream`` (None: the current one)."""
-    import contextlib
-
-    import torch
     if stream is None:
-        return contextlib.nullcontext()
+        return _HERE
+    torch = _torch()
     s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream))
     return torch.cuda.stream(s)
 
@@ -468,12 +494,12 @@ def embedding_lookup(ids, table, scale: float = 1.0, padding: int | None = None,
     """Rows of an embedding table by token: out[...] = scale * table[ids[...]], rounded once to ``dtype`` (fp32 or
     bf16; default: the table's), or into ``out`` (shape ids.shape + (dim,)). An id outside the table gives zeros and
     records MA_ERR_BOUNDS in the status word, except ``padding`` (-1, say), which only gives zeros."""
-    import torch
+    torch = _torch()
     _on_current_gpu("embedding_lookup", ids, table, out)
     ids, idt = _ids(ids, stream)
     if table.dim() != 2:
         raise MAError(MA_ERR_SHAPE, "embedding_lookup: the table must be 2-D")
-    V, D = (int(s) for s in table.shape)
+    V, D = table.shape
     tab, ldt = _rows(table, "embedding_lookup: table")
     if out is None:
         with _on_stream(stream):
@@ -502,12 +528,12 @@ def embedding_grad(ids, grad_rows, grad, scale: float = 1.0, padding: int | None
     reads) is written, zeros where no token points; with ``accumulate`` the sums are added to the rows that have
     tokens. fp32 sums in token order, no atomics: the same inputs give the same bits. Tokens equal to ``padding``
     add nothing. ws: workspace (embed_grad_workspace_bytes; allocated here when None). Returns ``grad``."""
-    import torch
+    torch = _torch()
     _on_current_gpu("embedding_grad", ids, grad_rows, grad, ws)
     ids, idt = _ids(ids, stream)
     if grad.dim() != 2 or grad_rows.shape != ids.shape + (grad.shape[1],):
         raise MAError(MA_ERR_SHAPE, "embedding_grad: grad must be rows x dim, grad_rows ids.shape + (dim,)")
-    V, D = (int(s) for s in grad.shape)
+    V, D = grad.shape
     g, ldg = _rows(grad, "embedding_grad: grad")
     y, ldy = _rows(grad_rows, "embedding_grad: grad_rows")
     need = embed_grad_workspace_bytes(ids.numel(), V, D)
@@ -579,15 +605,16 @@ def qk_max_logit(q, k, scale: float | None = None, causal: bool = True, offsets=
     with a number of heads that divides q's. dim: a multiple of 8 up to 256;
     strides multiples of 8. scale: default dim ** -0.5. ``accumulate`` takes the
     maximum with what ``out`` holds. Without a visible pair: -inf; a NaN logit: NaN."""
-    import torch
+    torch = _torch()
     _on_current_gpu("qk_max_logit", q, k, offsets, out)
     nd = 3 if offsets is not None else 4
     if q.dim() != nd or k.dim() != nd or q.shape[:-2] != k.shape[:-2] or q.shape[-1] != k.shape[-1]:
         raise MAError(MA_ERR_SHAPE, "qk_max_logit: q and k must be (sequences x) tokens x heads x dim")
     if q.dtype != torch.bfloat16 or k.dtype != torch.bfloat16:
         raise MAError(MA_ERR_DTYPE, "qk_max_logit: q and k must be bf16")
-    H, KV, D = int(q.shape[-2]), int(k.shape[-2]), int(q.shape[-1])
-    if q.numel() and (q.stride(-1) != 1 or k.stride(-1) != 1):
+    qt, kt = q.stride(), k.stride()
+    H, KV, D = q.shape[-2], k.shape[-2], q.shape[-1]
+    if (qt[-1] != 1 or kt[-1] != 1) and q.numel():
         raise MAError(MA_ERR_SHAPE, "qk_max_logit: dim must be contiguous")
     if accumulate and out is None:
         raise MAError(MA_ERR_NULL, "qk_max_logit: accumulate needs out")
@@ -599,13 +626,13 @@ def qk_max_logit(q, k, scale: float | None = None, causal: bool = True, offsets=
     if offsets is not None:
         if offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 1 or not offsets.is_contiguous():
             raise MAError(MA_ERR_SHAPE, "qk_max_logit: offsets must be sequences + 1 contiguous int32 positions")
-        S, total = offsets.numel() - 1, int(q.shape[0])
+        S, total = offsets.numel() - 1, q.shape[0]
         T, qs, ks = total if max_len is None else int(max_len), 0, 0
     else:
-        S, T, total = int(q.shape[0]), int(q.shape[1]), 0
-        qs, ks = int(q.stride(0)), int(k.stride(0))
-    _check(lib().ma_qk_max_logit(S, T, total, H, KV, D, _ptr(q), qs, int(q.stride(-3)), int(q.stride(-2)), _ptr(k), ks,
-                                 int(k.stride(-3)), int(k.stride(-2)), _ptr(offsets),
+        S, T, total = q.shape[0], q.shape[1], 0
+        qs, ks = qt[0], kt[0]
+    _check(lib().ma_qk_max_logit(S, T, total, H, KV, D, _ptr(q), qs, qt[-3], qt[-2], _ptr(k), ks, kt[-3], kt[-2],
+                                 _ptr(offsets),
                                  D ** -0.5 if scale is None else float(scale), int(bool(causal)), int(bool(absolute)),
                                  int(bool(accumulate)), _ptr(out), _stream(stream)), "qk_max_logit")
     return out
@@ -618,7 +645,7 @@ def qk_clip(wq, wk, max_logit, tau: float = 100.0, alpha: float = 0.5, kv_heads:
     factor to the power alpha, the key weights the rest; a key head shared by several query heads takes what the
     one furthest over needs, and its query heads' weights make up for it, so that each head's logits scale by its
     own factor. Heads within tau, or whose maximum is not finite, are not touched."""
-    import torch
+    torch = _torch()
     _on_current_gpu("qk_clip", wq, wk, max_logit)
     for t in (wq, wk, max_logit):
         if t.dtype != torch.float32:
@@ -769,6 +796,7 @@ class GradClip:
         self.grads = list(grads)
         _on_current_gpu("GradClip", *self.grads)
         self._tables = _grad_tables(self.grads)
+        self._args = (self._tables[0], *[ctypes.addressof(a) for a in self._tables[1:]])
         self.buffer = clip_buffer()
         self._norm = self.buffer[0]
         self._ptr = _ptr(self.buffer)
@@ -776,13 +804,13 @@ class GradClip:
     def norm(self, max_norm: float = math.inf, scale: float = 1.0, stream=None):
         """Fill ``buffer``; the norm (times scale) as a 0-d view of it, on the device. The next call overwrites it."""
         _on_current_gpu("GradClip.norm", self.buffer)
-        _check(lib().ma_grad_norm(*self._tables, scale, max_norm, self._ptr, _stream(stream)), "ma_grad_norm")
+        _check(lib().ma_grad_norm(*self._args, scale, max_norm, self._ptr, _stream(stream)), "ma_grad_norm")
         return self._norm
 
     def clip(self, max_norm: float, scale: float = 1.0, stream=None):
         """Scale and clip the gradients in place; returns their norm before clipping, as :meth:`norm` does."""
         _on_current_gpu("GradClip.clip", self.buffer)
-        _check(lib().ma_grad_clip(*self._tables, scale, max_norm, self._ptr, _stream(stream)), "ma_grad_clip")
+        _check(lib().ma_grad_clip(*self._args, scale, max_norm, self._ptr, _stream(stream)), "ma_grad_clip")
         return self._norm
 
 

@@ -53,7 +53,6 @@ __device__ __forceinline__ float load_g1(const void* g, int gdt, int64_t i) {
 template <bool CLIP>
 __global__ void __launch_bounds__(256) adamw_kernel(const __grid_constant__ AdamwLaunch L) {
     griddep_launch_dependents();
-    griddep_wait();
     const int64_t chunk = blockIdx.x;
     int lo = 0, hi = L.ntensors - 1;
     while (lo < hi) {  // last tensor whose first chunk is <= this chunk
@@ -63,6 +62,7 @@ __global__ void __launch_bounds__(256) adamw_kernel(const __grid_constant__ Adam
     }
     const AdamwTensorDesc& T = L.t[lo];
     const AdamwGroupConst H = L.grp[T.group];
+    griddep_wait();  // only the parameter block was read so far
     const float coef = CLIP ? L.clip->coef : 1.f;
     const int64_t start = (chunk - T.chunk0) * kAdamwChunk;
     if (start >= T.numel) return;

@@ -784,7 +784,7 @@ struct ma_plan {
         cudaGraphNode_t node;
         cudaKernelNodeParams params;  // func, launch shape; kernelParams replaced on update
         std::vector<uint8_t> arg;     // the kernel's single by-value parameter
-        int kind;                     // 0: AdamW launch, 1: Newton-Schulz final apply, 2: clip finalize
+        int kind;                     // 0: AdamW launch, 1: Newton-Schulz final apply, 2: norm and clipping coefficient
     };
     struct Graph {
         cudaGraph_t graph = nullptr;
@@ -1826,9 +1826,7 @@ int graph_patch(ma_plan* plan, const ma_group_t* groups) {
             const int st = ns_tc_patch_final(n.arg.data(), patch_final_job, &ctx);
             if (st) return st;
         } else if (n.kind == 2) {
-            ClipFinalize* F = reinterpret_cast<ClipFinalize*>(n.arg.data());
-            F->scale = plan->clip.scale;
-            F->max_norm = plan->clip.max_norm;
+            clip_patch(n.params.func, n.arg.data(), plan->clip.scale, plan->clip.max_norm);
         } else {
             AdamwLaunch* L = reinterpret_cast<AdamwLaunch*>(n.arg.data());
             for (int k = 0; k < ngroups; ++k) L->grp[k] = gc[k];
@@ -1909,9 +1907,9 @@ int graph_capture(ma_plan* plan, const ma_group_t* groups, void* ws, int sms, in
         }
         const bool adamw = is_adamw_kernel(p.func);
         const bool fin = ns_tc_is_final(p.func);
-        const bool clip = p.func == clip_finalize_func();
+        const size_t clip = clip_patch_bytes(p.func);
         if (!adamw && !fin && !clip) continue;
-        const size_t bytes = adamw ? sizeof(AdamwLaunch) : clip ? sizeof(ClipFinalize) : ns_tc_launch_bytes();
+        const size_t bytes = adamw ? sizeof(AdamwLaunch) : clip ? clip : ns_tc_launch_bytes();
         const uint8_t* a = reinterpret_cast<const uint8_t*>(p.kernelParams[0]);
         G.nodes.push_back({node, p, std::vector<uint8_t>(a, a + bytes), fin ? 1 : clip ? 2 : 0});
     }

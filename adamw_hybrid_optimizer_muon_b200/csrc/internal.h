@@ -108,7 +108,10 @@ struct GradItem {
 cudaError_t launch_grad_clip(const std::vector<GradItem>& items, const ClipArgs& args, int sms, bool in_place,
                              cudaStream_t s, int* launches);
 cudaError_t launch_clip_finalize(const ClipArgs& a, int nparts, cudaStream_t s);
-const void* clip_finalize_func();  // the kernel's host-side handle (CUDA-graph node matching)
+// CUDA-graph support: the size of the single (by value) parameter of a kernel that forms norm and coefficient (0:
+// another kernel), and an in-place update of the scale and the largest norm in it.
+size_t clip_patch_bytes(const void* func);
+void clip_patch(const void* func, void* arg, float scale, float max_norm);
 
 // ------------------------------------------------------------------ AdamW
 

@@ -28,6 +28,7 @@
 #include <climits>
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "common.cuh"
 #include "internal.h"
@@ -44,14 +45,48 @@ constexpr uint32_t kSmemMax = 232448;          // 227 KB
 constexpr uint32_t kCtlBytes = 512;
 constexpr int kMaxChunks = 4;                  // head dimension up to 256
 constexpr int kMaxStages = 12;
-constexpr uint32_t kSleepNs = 20000;
+// Stages of N keys x 64 columns that fit beside two blocks of queries of CH chunks.
+constexpr int stages(int n, int ch) {
+    const int fit = (int)((kSmemMax - 1024 - kCtlBytes - 2 * ch * kQChunk) / (uint32_t)(n * kBK * 2));
+    return fit < kMaxStages ? fit : kMaxStages;
+}
 constexpr long long kDrainNs = 50000000LL;  // bound of the waits for this CTA's own copies and MMAs at its end
+
+// Bounded wait for the phase with the given parity of a barrier: as
+// mbar_wait_ctl, for waits that are mostly over at once (wait) and, when not,
+// short. The timer is looked at only after 64 attempts that each slept up to
+// 1 us. False after the limit (recorded, and the abort raised) or, unless
+// `drain`, once another thread has raised the abort.
+struct Waits {
+    volatile int* abort;
+    long long limit_ns;
+    int* status;
+};
+__device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, const Waits& W, long long limit_ns, bool drain) {
+    for (int it = 0; it < 64; ++it) {
+        if (mbar_try_wait_sleep(bar, parity, 1000u)) return true;
+        if (!drain && *W.abort) return false;
+    }
+    const uint64_t t0 = globaltimer();
+    while (!mbar_try_wait_sleep(bar, parity, 1000u)) {
+        if (!drain && *W.abort) return false;
+        if ((long long)(globaltimer() - t0) > limit_ns) {
+            record_error(W.status, MA_ERR_TIMEOUT);
+            *W.abort = 1;
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Waits& W) {
+    return mbar_try_wait(bar, parity) || wait_on(bar, parity, W, W.limit_ns, false);
+}
 
 struct QkLaunch {
     CUtensorMap mq, mk;      // {dim, tokens, heads, sequences}
     const int32_t* offsets;  // packed: first token of each sequence and the end; NULL: sequences of `len` tokens
     int32_t seqs, len, total;  // len: tokens per sequence (packed: the longest); total: tokens of a packed batch
-    int32_t heads, kv, chunks, stages;
+    int32_t heads, kv;
     float scale;
     float* out;
     long long wait_limit_ns;
@@ -99,37 +134,29 @@ __device__ __forceinline__ int64_t units_of_head(int len) {
     return units_before<N, CAUSAL>((len + kRows - 1) / kRows, len);
 }
 
-// A part of one item (256 queries of a head): units [u0, u1) of it, in the order
-// key tile by key tile, the lower block of rows first.
+// The value of lane 0, known to be the same in every lane.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// A part of one item (256 queries of a head, in two blocks of 128): key tiles
+// [a0, b0) for the lower block of rows and [a1, b1) for the upper one, taken
+// tile by tile, the lower block first. Every tile from the first to the last
+// is used by a block.
 struct Segment {
     int b, h, q0, tok0, len;
-    int n0, n1;          // rows of the two blocks
-    int tiles0, tiles1;  // key tiles each of them sees
-    int u0, u1;
-    __device__ __forceinline__ void unit(int u, int& j, int& s) const {
-        if (n1 == 0) {
-            j = u;
-            s = 0;
-        } else if (u < 2 * tiles0) {
-            j = u >> 1;
-            s = u & 1;
-        } else {
-            j = u - tiles0;
-            s = 1;
-        }
-    }
-    // whether unit u is the first (last) of this segment that uses its key tile
-    __device__ __forceinline__ bool first_of_tile(int u) const {
-        return u == u0 || n1 == 0 || u >= 2 * tiles0 || (u & 1) == 0;
-    }
-    __device__ __forceinline__ bool last_of_tile(int u) const {
-        return u + 1 == u1 || n1 == 0 || u >= 2 * tiles0 || (u & 1) == 1;
-    }
-    __device__ __forceinline__ int count(int s) const {  // units of block s in [u0, u1)
-        if (n1 == 0) return s == 0 ? u1 - u0 : 0;
-        auto zeros = [&](int u) { return min(u, 2 * tiles0) + 1 >> 1; };  // units of block 0 before u
-        const int z = zeros(u1) - zeros(u0);
-        return s == 0 ? z : u1 - u0 - z;
+    int a0, b0, a1, b1;
+    __device__ __forceinline__ int first() const { return a0 < b0 && (a1 >= b1 || a0 <= a1) ? a0 : a1; }
+    __device__ __forceinline__ int last() const { return max(a0 < b0 ? b0 : 0, a1 < b1 ? b1 : 0); }
+    __device__ __forceinline__ bool in0(int j) const { return j >= a0 && j < b0; }
+    __device__ __forceinline__ bool in1(int j) const { return j >= a1 && j < b1; }
+    __device__ __forceinline__ void make_uniform() {
+        b = uniform(b);
+        h = uniform(h);
+        q0 = uniform(q0);
+        tok0 = uniform(tok0);
+        a0 = uniform(a0);
+        b0 = uniform(b0);
+        a1 = uniform(a1);
+        b1 = uniform(b1);
     }
 };
 
@@ -167,15 +194,19 @@ struct Walk {
         g.q0 = q * 2 * kRows;
         g.tok0 = sq.tok0;
         g.len = sq.len;
-        g.n0 = min(kRows, sq.len - g.q0);
-        g.n1 = max(0, min(kRows, sq.len - g.q0 - kRows));
+        const int n0 = min(kRows, sq.len - g.q0), n1 = max(0, min(kRows, sq.len - g.q0 - kRows));
         const int all = (sq.len + N - 1) / N;
-        g.tiles0 = CAUSAL ? (g.q0 + g.n0 + N - 1) / N : all;
-        g.tiles1 = g.n1 == 0 ? 0 : CAUSAL ? (g.q0 + kRows + g.n1 + N - 1) / N : all;
-        const int units = g.tiles0 + g.tiles1;
-        g.u0 = (int)(rest - item0);
-        g.u1 = (int)min((int64_t)units, g.u0 + left);
-        left -= g.u1 - g.u0;
+        const int tiles0 = CAUSAL ? (g.q0 + n0 + N - 1) / N : all;
+        const int tiles1 = n1 == 0 ? 0 : CAUSAL ? (g.q0 + kRows + n1 + N - 1) / N : all;
+        const int units = tiles0 + tiles1;
+        const int u0 = (int)(rest - item0), u1 = (int)min((int64_t)units, u0 + left);
+        left -= u1 - u0;
+        // units of the lower block before unit u: it has every other one, until its tiles end
+        auto lower = [&](int u) { return n1 == 0 ? u : (min(u, 2 * tiles0) + 1) >> 1; };
+        g.a0 = lower(u0);
+        g.b0 = lower(u1);
+        g.a1 = u0 - g.a0;
+        g.b1 = u1 - g.b0;
         // to the next item: the next 256 queries, the next head, the next sequence
         ++q;
         item0 += units;
@@ -193,13 +224,48 @@ struct Walk {
     }
 };
 
-// 4-D tiled load global -> shared, completing on `bar`.
-__device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1,
-                                            int c2, int c3) {
+// The loading and the MMA warp run their loops with all lanes together, every
+// value the same in each, and one elected lane issues. (Issued from inside a
+// one-lane branch, each MMA cost about 140 cycles of issue, more than its own
+// 128 x 256 x 16 product takes: operands of these instructions live in uniform
+// registers, which code for one lane of a divergent warp has to fill each time.)
+
+// 4-D tiled load global -> shared, completing on `bar`, after announcing its bytes there.
+__device__ __forceinline__ void load_4d(uint32_t smem_dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
+                                        int c3) {
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
-        "[%2];" ::"r"(smem_u32(smem_dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "@q cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
+        "[%2];\n\t}" ::"r"(smem_dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+        : "memory");
+}
+__device__ __forceinline__ void expect_bytes(uint32_t bar, uint32_t bytes) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+        "r"(bytes)
+        : "memory");
+}
+
+// D[tmem] (+)= A * B, as tc_mma_f16, issued by one lane of a converged warp.
+template <bool ACC>
+__device__ __forceinline__ void mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "n"(ACC ? 1 : 0)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
         : "memory");
 }
 
@@ -290,13 +356,20 @@ __device__ void find_share(const QkLaunch& L, QkCtl* ctl, int64_t* sums) {
     const int b0 = min(L.seqs, (int)threadIdx.x * per), b1 = min(L.seqs, b0 + per);
     int64_t mine = 0;
     for (int b = b0; b < b1; ++b) mine += units_of_seq<N, CAUSAL>(L, b);
-    sums[threadIdx.x] = mine;
+    int64_t upto = mine;  // of this warp's threads up to this one
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+        if ((int)(threadIdx.x & 31) >= o) upto += v;
+    }
+    if ((threadIdx.x & 31) == 31) sums[threadIdx.x >> 5] = upto;
     __syncthreads();
-    int64_t before = 0, total = 0;
-    for (int t = 0; t < kThreads; ++t) {
-        const int64_t v = sums[t];
-        if (t < (int)threadIdx.x) before += v;
-        total += v;
+    int64_t before = upto - mine;
+    int64_t total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < (int)(threadIdx.x >> 5)) before += sums[w];
+        total += sums[w];
     }
     const int64_t begin = total * blockIdx.x / gridDim.x, end = total * (blockIdx.x + 1) / gridDim.x;
     if (threadIdx.x == 0) {
@@ -320,20 +393,19 @@ __device__ void find_share(const QkLaunch& L, QkCtl* ctl, int64_t* sums) {
     __syncthreads();
 }
 
-template <int N, bool CAUSAL, bool ABS>
+template <int N, int CH, bool CAUSAL, bool ABS>
 __global__ void __launch_bounds__(kThreads, 1) qk_max_kernel(const __grid_constant__ QkLaunch L) {
     griddep_launch_dependents();
     constexpr uint32_t kStage = N * kBK * 2;
     constexpr int NB = 512 / N / 2;  // accumulators per block of rows
     extern __shared__ __align__(16) uint8_t raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) / 1024 * 1024);
-    const int chunks = L.chunks, nst = L.stages;
+    constexpr int nst = stages(N, CH);
     uint8_t* qbuf = smem;  // [block of rows][chunk]
-    uint8_t* ring = qbuf + 2 * chunks * kQChunk;
+    uint8_t* ring = qbuf + 2 * CH * kQChunk;
     QkCtl* ctl = reinterpret_cast<QkCtl*>(ring + nst * kStage);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const long long limit = L.wait_limit_ns;
-    const AbortCtl ab{&ctl->abort_flag, 0u};
+    const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
+    const Waits W{&ctl->abort_flag, L.wait_limit_ns, L.status};
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < nst; ++s) {
@@ -367,124 +439,121 @@ __global__ void __launch_bounds__(kThreads, 1) qk_max_kernel(const __grid_consta
     fence_proxy_async_smem();
     __syncthreads();
 
+    // shared-memory addresses: the same expressions in every lane
+    const uint32_t q_base = smem_u32(qbuf), ring_base = smem_u32(ring);
+    const uint32_t full_bar = smem_u32(&ctl->full[0]), empty_bar = smem_u32(&ctl->empty[0]);
+    const uint32_t q_full_bar = smem_u32(&ctl->q_full[0]), q_empty_bar = smem_u32(&ctl->q_empty[0]);
+    const uint32_t acc_full_bar = smem_u32(&ctl->acc_full[0]), acc_empty_bar = smem_u32(&ctl->acc_empty[0]);
     if (warp == 0) {
-        if (lane == 0) {
-            int stage = 0, uses = 0;
-            uint32_t phase = 0;
-            int q_uses[2] = {0, 0};
-            bool ok = true;
-            Walk<N, CAUSAL> walk(L, ctl);
-            Segment g;
-            while (ok && walk.next(g)) {
-                const int kvh = g.h / (L.heads / L.kv);
-                auto load_q = [&](int s) {
-                    if (!mbar_wait_ctl(&ctl->q_empty[s], (q_uses[s] & 1u) ^ 1u, ab, limit, L.status)) return false;
-                    ++q_uses[s];
-                    mbar_arrive_expect_tx(&ctl->q_full[s], chunks * kQChunk);
-                    for (int c = 0; c < chunks; ++c)
-                        tma_load_4d(qbuf + (s * chunks + c) * kQChunk, &L.mq, &ctl->q_full[s], c * kBK,
-                                    g.tok0 + g.q0 + s * kRows, g.h, g.b);
-                    return true;
-                };
-                bool need_q[2] = {g.count(0) > 0, g.count(1) > 0};
-                for (int u = g.u0; u < g.u1 && ok; ++u) {
-                    int j, s;
-                    g.unit(u, j, s);
-                    if (need_q[s]) {  // in the order the MMAs use them
-                        need_q[s] = false;
-                        if (!(ok = load_q(s))) break;
-                    }
-                    if (!g.first_of_tile(u)) continue;
-                    for (int c = 0; c < chunks; ++c) {
-                        if (!mbar_wait_ctl(&ctl->empty[stage], phase ^ 1u, ab, limit, L.status)) {
-                            ok = false;
-                            break;
-                        }
-                        mbar_arrive_expect_tx(&ctl->full[stage], kStage);
-                        tma_load_4d(ring + stage * kStage, &L.mk, &ctl->full[stage], c * kBK, g.tok0 + j * N, kvh, g.b);
-                        ++uses;
-                        if (++stage == nst) {
-                            stage = 0;
-                            phase ^= 1u;
-                        }
-                    }
-                }
-            }
-            // every copy of this CTA has landed before it exits (an abort leaves some unread)
-            for (int s = 0; s < nst; ++s) {
-                const int n = uses / nst + (s < uses % nst ? 1 : 0);  // uses of stage s
-                if (n > 0) mbar_wait_ctl(&ctl->full[s], (n - 1) & 1u, ab, kDrainNs, L.status, 0, false, true);
-            }
-            for (int s = 0; s < 2; ++s)
-                if (q_uses[s] > 0)
-                    mbar_wait_ctl(&ctl->q_full[s], (q_uses[s] - 1) & 1u, ab, kDrainNs, L.status, 0, false, true);
-        }
-    } else if (warp == 1) {
-        if (lane == 0) {
-            constexpr uint32_t IDESC = idesc_bf16_f32(kRows, N, 0);
-            int stage = 0;
-            uint32_t phase = 0;
-            int q_uses[2] = {0, 0}, acc_uses[2] = {0, 0};
-            bool ok = true;
-            Walk<N, CAUSAL> walk(L, ctl);
-            Segment g;
-            while (ok && walk.next(g)) {
-                int left[2] = {g.count(0), g.count(1)};
-                bool fresh[2] = {true, true};
-                for (int u = g.u0; u < g.u1 && ok; ++u) {
-                    int j, s;
-                    g.unit(u, j, s);
-                    const int a = s * NB + acc_uses[s] % NB;
-                    if (!mbar_wait_ctl(&ctl->acc_empty[a], ((acc_uses[s] / NB) & 1u) ^ 1u, ab, limit, L.status)) {
-                        ok = false;
-                        break;
-                    }
-                    if (fresh[s]) {
-                        fresh[s] = false;
-                        if (!mbar_wait_ctl(&ctl->q_full[s], q_uses[s] & 1u, ab, limit, L.status)) {
-                            ok = false;
-                            break;
-                        }
-                        ++q_uses[s];
-                    }
-                    tc_fence_after();
-                    const bool first = g.first_of_tile(u), last = g.last_of_tile(u);
-                    const uint32_t d = tmem + (uint32_t)(a * N);
-                    int st = stage;
-                    uint32_t ph = phase;
-                    for (int c = 0; c < chunks; ++c) {
-                        if (first) {
-                            if (!mbar_wait_ctl(&ctl->full[st], ph, ab, limit, L.status)) {
-                                ok = false;
-                                break;
-                            }
-                            tc_fence_after();
-                        }
-                        const uint32_t a0 = smem_u32(qbuf + (s * chunks + c) * kQChunk);
-                        const uint32_t b0 = smem_u32(ring + st * kStage);
+        int stage = 0, uses = 0, q_uses0 = 0, q_uses1 = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        Walk<N, CAUSAL> walk(L, ctl);
+        Segment g;
+        while (ok && walk.next(g)) {
+            g.make_uniform();
+            const int kvh = g.h / (L.heads / L.kv);
+            auto load_q = [&](int s, int& n) {
+                if (!wait(q_empty_bar + 8 * s, (n & 1u) ^ 1u, W)) return false;
+                ++n;
+                expect_bytes(q_full_bar + 8 * s, CH * kQChunk);
 #pragma unroll
-                        for (int kk = 0; kk < kBK / 16; ++kk)
-                            tc_mma_f16(d, smem_desc_sw128(a0 + kk * 32, 16, 1024), smem_desc_sw128(b0 + kk * 32, 16, 1024),
-                                       IDESC, (c | kk) != 0 ? 1u : 0u);
-                        if (last) tc_commit(&ctl->empty[st]);
-                        if (++st == nst) {
-                            st = 0;
-                            ph ^= 1u;
-                        }
+                for (int c = 0; c < CH; ++c)
+                    load_4d(q_base + (s * CH + c) * kQChunk, &L.mq, q_full_bar + 8 * s, c * kBK,
+                            g.tok0 + g.q0 + s * kRows, g.h, g.b);
+                return true;
+            };
+            const int end = g.last();
+            for (int j = g.first(); j < end && ok; ++j) {
+                // in the order the MMAs take them: lower queries, keys, upper queries
+                const bool in0 = g.in0(j), q1 = g.in1(j) && j == g.a1;
+                if (in0 && j == g.a0) ok = load_q(0, q_uses0);
+                if (ok && !in0 && q1) ok = load_q(1, q_uses1);
+#pragma unroll
+                for (int c = 0; c < CH; ++c) {
+                    if (!ok || !(ok = wait(empty_bar + 8 * stage, phase ^ 1u, W))) break;
+                    expect_bytes(full_bar + 8 * stage, kStage);
+                    load_4d(ring_base + stage * kStage, &L.mk, full_bar + 8 * stage, c * kBK, g.tok0 + j * N, kvh, g.b);
+                    ++uses;
+                    if (++stage == nst) {
+                        stage = 0;
+                        phase ^= 1u;
                     }
-                    if (!ok) break;
-                    if (last) {
-                        stage = st;
-                        phase = ph;
-                    }
-                    ++acc_uses[s];
-                    if (--left[s] == 0) tc_commit(&ctl->q_empty[s]);
-                    tc_commit(&ctl->acc_full[a]);
+                }
+                if (ok && in0 && q1) ok = load_q(1, q_uses1);
+            }
+        }
+        // every copy of this CTA has landed before it exits (an abort leaves some unread)
+        for (int s = 0; s < nst; ++s) {
+            const int n = uses / nst + (s < uses % nst ? 1 : 0);  // uses of stage s
+            if (n > 0) wait_on(full_bar + 8 * s, (n - 1) & 1u, W, kDrainNs, true);
+        }
+        if (q_uses0 > 0) wait_on(q_full_bar, (q_uses0 - 1) & 1u, W, kDrainNs, true);
+        if (q_uses1 > 0) wait_on(q_full_bar + 8, (q_uses1 - 1) & 1u, W, kDrainNs, true);
+    } else if (warp == 1) {
+        // The MMA queue is a few products deep: what this warp does between the products of one block of rows
+        // and the next has to fit in the time of about three of them.
+        constexpr uint32_t IDESC = idesc_bf16_f32(kRows, N, 0);
+        const uint64_t desc = smem_desc_sw128(0, 16, 1024);  // plus an address in 16-byte units
+        const uint64_t qd = desc + (q_base >> 4);
+        int stage = 0, q_uses0 = 0, q_uses1 = 0, acc0 = 0, acc1 = 0;  // uses of each block's queries, accumulators
+        uint32_t phase = 0;
+        bool ok = true;
+        Walk<N, CAUSAL> walk(L, ctl);
+        Segment g;
+        // the products of block S with the key tile at the ring's stage; `first`: its copies are waited for,
+        // `last`: its stages are released
+        auto block = [&](auto which, int& uses, int& q_uses, bool fresh, bool first, bool last, bool done) {
+            constexpr int S = decltype(which)::value;
+            const int a = S * NB + (NB == 1 ? 0 : uses & (NB - 1));
+            if (!wait(acc_empty_bar + 8 * a, ((uses / NB) & 1u) ^ 1u, W)) return false;
+            ++uses;
+            if (fresh) {
+                if (!wait(q_full_bar + 8 * S, q_uses & 1u, W)) return false;
+                ++q_uses;
+            }
+            const uint32_t d = tmem + (uint32_t)(a * N);
+            int st = stage;
+            uint32_t ph = phase;
+            if (!first) tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < CH; ++c) {
+                if (first) {
+                    if (!wait(full_bar + 8 * st, ph, W)) return false;
+                    tc_fence_after();
+                }
+                const uint64_t ad = qd + (((S * CH + c) * kQChunk) >> 4), bd = desc + ((ring_base + st * kStage) >> 4);
+                if (c == 0) mma_f16<false>(d, ad, bd, IDESC);
+                else mma_f16<true>(d, ad, bd, IDESC);
+#pragma unroll
+                for (int kk = 1; kk < kBK / 16; ++kk) mma_f16<true>(d, ad + 2 * kk, bd + 2 * kk, IDESC);
+                if (last) commit(empty_bar + 8 * st);
+                if (++st == nst) {
+                    st = 0;
+                    ph ^= 1u;
                 }
             }
-            tc_commit(&ctl->drain);  // every MMA has read its operands before this CTA exits
-            mbar_wait_ctl(&ctl->drain, 0, ab, kDrainNs, L.status, 0, false, true);
+            if (last) {
+                stage = st;
+                phase = ph;
+            }
+            commit(acc_full_bar + 8 * a);
+            if (done) commit(q_empty_bar + 8 * S);
+            return true;
+        };
+        while (ok && walk.next(g)) {
+            g.make_uniform();
+            const int end = g.last();
+            for (int j = g.first(); j < end && ok; ++j) {
+                const bool in0 = g.in0(j), in1 = g.in1(j);
+                if (in0)
+                    ok = block(std::integral_constant<int, 0>{}, acc0, q_uses0, j == g.a0, true, !in1, j + 1 == g.b0);
+                if (ok && in1)
+                    ok = block(std::integral_constant<int, 1>{}, acc1, q_uses1, j == g.a1, !in0, true, j + 1 == g.b1);
+            }
         }
+        commit(smem_u32(&ctl->drain));  // every MMA has read its operands before this CTA exits
+        wait_on(smem_u32(&ctl->drain), 0, W, kDrainNs, true);
     } else {
         const int quad = warp & 3, s = (warp - 2) >> 2;
         const uint32_t lane_base = tmem + ((uint32_t)(quad * 32) << 16);
@@ -496,19 +565,10 @@ __global__ void __launch_bounds__(kThreads, 1) qk_max_kernel(const __grid_consta
             const int i = g.q0 + s * kRows + quad * 32 + lane;  // this thread's query
             const int lim = i >= g.len ? -1 : CAUSAL ? i : g.len - 1;  // its last visible key
             float m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            bool any = false;
-            for (int u = g.u0; u < g.u1; ++u) {
-                int j, us;
-                g.unit(u, j, us);
-                if (us != s) continue;
-                any = true;
-                const int a = s * NB + uses % NB;
-                int got = 1;
-                if (lane == 0) got = mbar_wait_ctl(&ctl->acc_full[a], (uses / NB) & 1u, ab, limit, L.status, kSleepNs);
-                if (!__shfl_sync(0xffffffffu, got, 0)) {
-                    ok = false;
-                    break;
-                }
+            const int j0 = s ? g.a1 : g.a0, j1 = s ? g.b1 : g.b0;
+            for (int j = j0; j < j1; ++j) {
+                const int a = s * NB + (NB == 1 ? 0 : uses & (NB - 1));
+                if (!(ok = wait(acc_full_bar + 8 * a, (uses / NB) & 1u, W))) break;
                 tc_fence_after();
                 const uint32_t t0 = lane_base + (uint32_t)(a * N);
                 const int n = lim - j * N + 1;  // columns of this tile the query sees
@@ -538,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1) qk_max_kernel(const __grid_consta
                 if (lane == 0) mbar_arrive(&ctl->acc_empty[a]);
                 ++uses;
             }
-            if (!ok || !any) continue;
+            if (!ok || j0 >= j1) continue;
             float v = max_nan(max_nan(m[0], m[1]), max_nan(m[2], m[3]));
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -582,20 +642,22 @@ __device__ __forceinline__ float share(float g, float e) { return g == 1.f ? 1.f
 
 // Every block lists the heads whose factor is not 1, then takes its share of
 // their pieces. A head within the threshold costs nothing.
-__global__ void __launch_bounds__(kScaleThreads) qk_scale_kernel(const __grid_constant__ QkScale A) {
+__global__ void __launch_bounds__(kScaleThreads, 4) qk_scale_kernel(const __grid_constant__ QkScale A) {
     griddep_launch_dependents();
     griddep_wait();
     __shared__ float factor[kMaxHeads];
     __shared__ int16_t list[kMaxHeads];
     __shared__ int count[2];
     const int group = A.heads / A.kv;
+    for (int h = threadIdx.x; h < A.heads; h += kScaleThreads) factor[h] = gamma_of(A.top[h], A.tau);
+    __syncthreads();
     for (int c = threadIdx.x; c < A.kv; c += kScaleThreads) {
         float least = 1.f;
-        for (int k = 0; k < group; ++k) least = fminf(least, gamma_of(A.top[c * group + k], A.tau));
+        for (int k = 0; k < group; ++k) least = fminf(least, factor[c * group + k]);
         const float fk = share(least, 1.f - A.alpha);
         factor[A.heads + c] = fk;
         for (int k = 0; k < group; ++k) {
-            const float g = gamma_of(A.top[c * group + k], A.tau);
+            const float g = factor[c * group + k];
             // without shared heads this is g^alpha; formed as the quotient so that the two factors multiply to g
             factor[c * group + k] = group == 1 ? share(g, A.alpha) : g / fk;
         }
@@ -627,12 +689,18 @@ __global__ void __launch_bounds__(kScaleThreads) qk_scale_kernel(const __grid_co
         [[maybe_unused]] const int64_t end = isq ? A.heads * A.nq : A.kv * A.nk;
         const float f = factor[h];
         if (A.vec) {
-#pragma unroll 8
-            for (int64_t i = i0 + 4 * threadIdx.x; i < i1; i += 4 * kScaleThreads) {
-                if (!MA_INB(at + i, 4, end, A.status)) continue;
-                float4 x = *reinterpret_cast<const float4*>(w + i);
-                x.x *= f; x.y *= f; x.z *= f; x.w *= f;
-                *reinterpret_cast<float4*>(w + i) = x;
+            constexpr int U = kScaleChunk / (4 * kScaleThreads);  // every load of the piece before the first store
+            float4 x[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t i = i0 + 4 * (threadIdx.x + u * kScaleThreads);
+                if (i < i1 && MA_INB(at + i, 4, end, A.status)) x[u] = __ldcs(reinterpret_cast<const float4*>(w + i));
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t i = i0 + 4 * (threadIdx.x + u * kScaleThreads);
+                if (i < i1 && MA_INB(at + i, 4, end, A.status))
+                    __stcs(reinterpret_cast<float4*>(w + i), make_float4(x[u].x * f, x[u].y * f, x[u].z * f, x[u].w * f));
             }
         } else {
             for (int64_t i = i0 + threadIdx.x; i < i1; i += kScaleThreads)
@@ -672,25 +740,27 @@ bool make_map(CUtensorMap* map, const void* base, int64_t dim, int64_t tokens, i
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int N, bool CAUSAL, bool ABS>
-cudaError_t launch_max(const QkLaunch& L, int grid, uint32_t smem, cudaStream_t s) {
+template <int N, int CH, bool CAUSAL, bool ABS>
+cudaError_t launch_max(const QkLaunch& L, int grid, cudaStream_t s) {
+    static_assert(stages(N, CH) >= CH, "a key tile has to fit in the ring");
+    constexpr uint32_t smem = 1024 + 2 * CH * kQChunk + stages(N, CH) * N * kBK * 2 + kCtlBytes;
     static PerDevice<int> cache;
     int dev = 0, done = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     e = cache.get(dev, &done, [](int* v) {
         *v = 1;
-        return cudaFuncSetAttribute(qk_max_kernel<N, CAUSAL, ABS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    (int)kSmemMax);
+        return cudaFuncSetAttribute(qk_max_kernel<N, CH, CAUSAL, ABS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)smem);
     });
     if (e != cudaSuccess) return e;
-    return launch_pdl(qk_max_kernel<N, CAUSAL, ABS>, dim3(grid), dim3(kThreads), smem, s, L);
+    return launch_pdl(qk_max_kernel<N, CH, CAUSAL, ABS>, dim3(grid), dim3(kThreads), smem, s, L);
 }
 
-template <int N>
-cudaError_t launch_max_n(const QkLaunch& L, bool causal, bool abs, int grid, uint32_t smem, cudaStream_t s) {
-    if (causal) return abs ? launch_max<N, true, true>(L, grid, smem, s) : launch_max<N, true, false>(L, grid, smem, s);
-    return abs ? launch_max<N, false, true>(L, grid, smem, s) : launch_max<N, false, false>(L, grid, smem, s);
+template <int N, int CH>
+cudaError_t launch_max_ch(const QkLaunch& L, bool causal, bool abs, int grid, cudaStream_t s) {
+    if (causal) return abs ? launch_max<N, CH, true, true>(L, grid, s) : launch_max<N, CH, true, false>(L, grid, s);
+    return abs ? launch_max<N, CH, false, true>(L, grid, s) : launch_max<N, CH, false, false>(L, grid, s);
 }
 
 // Keys per tile: 256, or 128 for head dimensions above 192, whose key tile of
@@ -735,7 +805,7 @@ int qk_max(int64_t seqs, int64_t len, int64_t total, int heads, int kv_heads, in
     QkLaunch L;
     std::memset(&L, 0, sizeof(L));
     const int n = tile_keys(dim);
-    L.chunks = (dim + kBK - 1) / kBK;
+    const int chunks = (dim + kBK - 1) / kBK;
     if (work) {
         // a stride of an extent of 1 is never followed, but the map wants one of at least 16 bytes
         auto fix = [&](int64_t x) { return x > 0 ? x : (int64_t)8 * ((dim + 7) / 8); };
@@ -758,9 +828,6 @@ int qk_max(int64_t seqs, int64_t len, int64_t total, int heads, int kv_heads, in
         L.out = out;
         L.wait_limit_ns = host_wait_limit_ns();
         L.status = device_status_ptr();
-        const uint32_t qbytes = 2 * L.chunks * kQChunk, stage = n * kBK * 2;
-        L.stages = std::min<int>(kMaxStages, (int)((kSmemMax - 1024 - kCtlBytes - qbytes) / stage));
-        const uint32_t smem = 1024 + qbytes + L.stages * stage + kCtlBytes;
         // a CTA per SM; fewer when there are fewer units (dense batches: the host knows)
         int grid = sms;
         if (!offsets) {
@@ -770,8 +837,10 @@ int qk_max(int64_t seqs, int64_t len, int64_t total, int heads, int kv_heads, in
             grid = (int)std::min<int64_t>(sms, units * std::min<int64_t>(seqs, sms));
             flops = 2.0 * dim * heads * (double)seqs * (causal ? 0.5 * len * (len + 1.0) : (double)len * len);
         }
-        e = n == 256 ? launch_max_n<256>(L, causal, absolute, grid, smem, s)
-                     : launch_max_n<128>(L, causal, absolute, grid, smem, s);
+        e = chunks == 1   ? launch_max_ch<256, 1>(L, causal, absolute, grid, s)
+            : chunks == 2 ? launch_max_ch<256, 2>(L, causal, absolute, grid, s)
+            : chunks == 3 ? launch_max_ch<256, 3>(L, causal, absolute, grid, s)
+                          : launch_max_ch<128, 4>(L, causal, absolute, grid, s);
     }
     prof_end(pr, s, flops, 0.0);
     return e == cudaSuccess ? MA_OK : MA_ERR_CUDA;
