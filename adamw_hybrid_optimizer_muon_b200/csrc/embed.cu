@@ -12,18 +12,22 @@
 //
 // Sort. Keys are token ids; positions of the batch travel with them. Up to
 // 8192 tokens of a table of fewer than 2^19 rows are sorted by one block in
-// shared memory, key and position packed into 32 bits; more by tiles of 4096,
-// a histogram and a scatter launch per digit, each scatter block forming its
-// own offsets from the tiles' histograms. Digits have up to nine bits, so a
-// vocabulary below 2^18 takes two passes. A bit map of the rows that have
-// tokens is filled on the way.
+// shared memory, key and position packed into 32 bits; more by tiles of 1024, a
+// histogram, a scan and a scatter launch per digit. Digits have up to nine bits:
+// a vocabulary below 2^18 takes two passes.
 //
-// Sum. The sorted tokens are cut into tiles of S. A block of 128 threads takes
-// one tile and 128 * VEC columns and walks the tile with eight rows' loads in
-// flight; a run of equal tokens inside the tile is written to its row at once.
-// A run that crosses tiles leaves one fp32 partial row per tile, and a second
-// kernel adds those in tile order. Other blocks of the same launch write zeros
-// to the rows that have no token.
+// Sum. The sorted tokens are cut into tiles of S. A block takes one tile and a
+// range of columns and adds up the runs of equal tokens that begin in its tile,
+// to their ends if those lie beyond it, with four to eight rows' loads in
+// flight per thread. Only a run of more than kLong tokens is cut at the tiles'
+// borders: each tile leaves an fp32 partial row, and a last kernel adds those
+// in tile order.
+//
+// Zeros. Most of a table's rows have no token, and writing their zeros is most
+// of the traffic. The sort and the last kernel are bound by latency and leave
+// HBM idle, so the zeros are spread: each kernel from the one that knows which
+// rows have tokens on (a bit per row) writes a share beside its own work, the
+// sums the rest.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -44,12 +48,14 @@ constexpr int kPosBits = 13;
 constexpr int kSmallKeyBits = 32 - kPosBits;
 constexpr int kMaxDigitBits = 9;
 constexpr int kMaxDigits = 1 << kMaxDigitBits;
-constexpr int kTileThreads = 512;
+constexpr int kTileThreads = 128;
 constexpr int kTile = kTileThreads * 8;  // tokens a block ranks at a time
-constexpr int kMaxTiles = 512;           // histograms a scatter block reads per digit
-constexpr int kSumThreads = 128;
+constexpr int kMaxTiles = 4096;          // tiles of a pass; longer batches have longer tiles
+constexpr int kSumThreads = 256;         // at most
 constexpr int kFixThreads = 256;
-constexpr int kRowsAhead = 8;            // rows of dY whose loads are in flight per thread
+constexpr int kMaxSumTile = 64;
+constexpr int kRing = 16;                // 16-byte copies in flight per thread of the sums
+constexpr int kLong = 32;                // tokens; a longer run is cut at the tiles' borders
 
 struct Ids {
     const void* p;
@@ -58,17 +64,38 @@ struct Ids {
     int* status;
 };
 
-// The sort key of token i: its id, or `rows` for one that adds to no row
+// The sort key of an id: itself, or `rows` for one that adds to no row
 // (padding, or an id outside the table, which is recorded).
-__device__ __forceinline__ uint32_t id_key(const Ids& I, int64_t i) {
-    if (!MA_INB(i, 1, I.n, I.status)) return (uint32_t)I.rows;
-    const int64_t id = I.i64 ? reinterpret_cast<const int64_t*>(I.p)[i] : reinterpret_cast<const int32_t*>(I.p)[i];
+__device__ __forceinline__ uint32_t id_key(const Ids& I, int64_t id) {
     if (id == I.padding) return (uint32_t)I.rows;
     if (id < 0 || id >= I.rows) {
         record_error(I.status, MA_ERR_BOUNDS);
         return (uint32_t)I.rows;
     }
     return (uint32_t)id;
+}
+
+// Keys of tokens first, first + stride, ... (R of them, `none` from `end` on):
+// every load before the first use.
+template <int R>
+__device__ __forceinline__ void load_keys(const Ids& I, int64_t first, int64_t stride, int64_t end, uint32_t none,
+                                          uint32_t (&key)[R]) {
+    int64_t id[R];
+    if (I.i64) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t i = first + r * stride;
+            id[r] = i < end && MA_INB(i, 1, I.n, I.status) ? reinterpret_cast<const int64_t*>(I.p)[i] : I.padding;
+        }
+    } else {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t i = first + r * stride;
+            id[r] = i < end && MA_INB(i, 1, I.n, I.status) ? reinterpret_cast<const int32_t*>(I.p)[i] : I.padding;
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) key[r] = first + r * stride < end ? id_key(I, id[r]) : none;
 }
 
 // Lanes of the warp (among `valid`) whose digit equals this lane's.
@@ -106,212 +133,6 @@ __device__ __forceinline__ uint32_t digit_scan(uint32_t total, uint32_t* warp_su
     __syncthreads();
     return x - total + (w ? warp_sums[w - 1] : 0);
 }
-
-struct SortArgs {
-    Ids ids;
-    uint32_t* keys;    // out: sorted keys
-    int32_t* pos;      // out: their positions
-    uint32_t* bitmap;  // rows that have tokens
-    int32_t bitmap_words;
-    int32_t digit_bits, passes;
-};
-
-// One block sorts up to 8192 tokens. Warp w owns items 256 w .. 256 w + 255, in
-// eight rounds of 32; the rank of an item among the equal digits of its warp is
-// the warp's running count of that digit plus the equal lanes before it.
-__global__ void __launch_bounds__(kSortThreads) embed_sort_small_kernel(const __grid_constant__ SortArgs A) {
-    griddep_launch_dependents();
-    griddep_wait();
-    extern __shared__ uint32_t smem[];
-    uint32_t* items = smem;                                                  // 8192
-    uint16_t* hist = reinterpret_cast<uint16_t*>(smem + kSmallSort);         // [32][ndig]
-    __shared__ uint32_t warp_sums[32];
-    __shared__ uint32_t base[kMaxDigits];
-    const int t = threadIdx.x, lane = t & 31, w = t >> 5;
-    const int n = (int)A.ids.n, ndig = 1 << A.digit_bits;
-    for (int i = t; i < A.bitmap_words; i += kSortThreads) A.bitmap[i] = 0;
-    uint32_t item[kSortItems];
-#pragma unroll
-    for (int r = 0; r < kSortItems; ++r) {
-        const int i = w * (32 * kSortItems) + 32 * r + lane;
-        item[r] = i < n ? (id_key(A.ids, i) << kPosBits) | (uint32_t)i : 0xffffffffu;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < kSortItems; ++r) {
-        const uint32_t key = item[r] >> kPosBits;
-        if (item[r] != 0xffffffffu && key < (uint32_t)A.ids.rows && MA_INB(key >> 5, 1, A.bitmap_words, A.ids.status))
-            atomicOr(&A.bitmap[key >> 5], 1u << (key & 31));
-    }
-    for (int p = 0; p < A.passes; ++p) {
-        const int shift = kPosBits + p * A.digit_bits;
-        for (int i = t; i < 16 * ndig; i += kSortThreads) reinterpret_cast<uint32_t*>(hist)[i] = 0;
-        __syncthreads();
-        uint32_t rank[kSortItems];
-#pragma unroll
-        for (int r = 0; r < kSortItems; ++r) {
-            const uint32_t d = (item[r] >> shift) & (ndig - 1);
-            const uint32_t peers = match_digit(d, A.digit_bits, 0xffffffffu);
-            const uint32_t before = hist[w * ndig + d];
-            rank[r] = before + __popc(peers & ((1u << lane) - 1));
-            __syncwarp();
-            if (lane == __ffs(peers) - 1) hist[w * ndig + d] = (uint16_t)(before + __popc(peers));
-            __syncwarp();
-        }
-        __syncthreads();
-        uint32_t total = 0;
-        if (t < ndig) {
-            for (int q = 0; q < kSortThreads / 32; ++q) {
-                const uint32_t c = hist[q * ndig + t];
-                hist[q * ndig + t] = (uint16_t)total;
-                total += c;
-            }
-        }
-        const uint32_t excl = digit_scan<kSortThreads>(total, warp_sums);
-        if (t < ndig) base[t] = excl;
-        __syncthreads();
-#pragma unroll
-        for (int r = 0; r < kSortItems; ++r) {
-            const uint32_t d = (item[r] >> shift) & (ndig - 1);
-            items[base[d] + hist[w * ndig + d] + rank[r]] = item[r];
-        }
-        __syncthreads();
-        if (p + 1 < A.passes) {
-#pragma unroll
-            for (int r = 0; r < kSortItems; ++r) item[r] = items[w * (32 * kSortItems) + 32 * r + lane];
-        }
-    }
-    for (int i = t; i < n; i += kSortThreads) {
-        A.keys[i] = items[i] >> kPosBits;
-        A.pos[i] = (int32_t)(items[i] & ((1u << kPosBits) - 1));
-    }
-}
-
-struct TileArgs {
-    Ids ids;
-    const uint32_t* kin;  // NULL: the first pass, keys from the ids
-    const int32_t* pin;
-    uint32_t* kout;
-    int32_t* pout;
-    uint32_t* hist;       // [tiles][digits]
-    uint32_t* bitmap;
-    int32_t bitmap_words;
-    int32_t shift, digit_bits, tiles, subtiles;  // a block ranks `subtiles` runs of kTile tokens, one after the other
-};
-
-__device__ __forceinline__ uint32_t tile_key(const TileArgs& A, int64_t i) {
-    return A.kin ? A.kin[i] : id_key(A.ids, i);
-}
-
-__global__ void __launch_bounds__(kTileThreads) embed_hist_kernel(const __grid_constant__ TileArgs A) {
-    griddep_launch_dependents();
-    griddep_wait();
-    __shared__ uint32_t h[kMaxDigits];
-    const int ndig = 1 << A.digit_bits;
-    for (int i = threadIdx.x; i < ndig; i += kTileThreads) h[i] = 0;
-    if (!A.kin)  // the first pass clears the map, the first scatter fills it
-        for (int i = blockIdx.x * kTileThreads + threadIdx.x; i < A.bitmap_words; i += gridDim.x * kTileThreads)
-            A.bitmap[i] = 0;
-    __syncthreads();
-    const int64_t i0 = (int64_t)blockIdx.x * A.subtiles * kTile;
-    const int64_t i1 = min(A.ids.n, i0 + (int64_t)A.subtiles * kTile);
-    for (int64_t i = i0 + threadIdx.x; i < i1; i += kTileThreads)
-        atomicAdd(&h[(tile_key(A, i) >> A.shift) & (ndig - 1)], 1u);
-    __syncthreads();
-    for (int i = threadIdx.x; i < ndig; i += kTileThreads) A.hist[(int64_t)blockIdx.x * ndig + i] = h[i];
-}
-
-__global__ void __launch_bounds__(kTileThreads) embed_scatter_kernel(const __grid_constant__ TileArgs A) {
-    griddep_launch_dependents();
-    griddep_wait();
-    constexpr int W = kTileThreads / 32;
-    __shared__ __align__(16) uint16_t hist[W * kMaxDigits];
-    __shared__ uint32_t base[kMaxDigits];
-    __shared__ uint32_t warp_sums[32];
-    const int t = threadIdx.x, lane = t & 31, w = t >> 5;
-    const int ndig = 1 << A.digit_bits;
-    // where this block's tokens of digit t begin: all smaller digits, and this digit in the tiles before
-    uint32_t total = 0, mine = 0;
-    if (t < ndig) {
-#pragma unroll 8
-        for (int q = 0; q < A.tiles; ++q) {
-            const uint32_t c = A.hist[(int64_t)q * ndig + t];
-            if (q < (int)blockIdx.x) mine += c;
-            total += c;
-        }
-    }
-    const uint32_t excl = digit_scan<kTileThreads>(total, warp_sums);
-    if (t < ndig) base[t] = excl + mine;
-    for (int sub = 0; sub < A.subtiles; ++sub) {
-        const int64_t i0 = ((int64_t)blockIdx.x * A.subtiles + sub) * kTile;
-        if (i0 >= A.ids.n) break;
-        for (int i = t; i < W * ndig / 2; i += kTileThreads) reinterpret_cast<uint32_t*>(hist)[i] = 0;
-        __syncthreads();
-        uint32_t key[8], rank[8];
-        int32_t pos[8];
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            const int64_t i = i0 + w * 256 + 32 * r + lane;
-            const bool in = i < A.ids.n;
-            key[r] = in ? tile_key(A, i) : 0u;
-            pos[r] = in ? (A.pin ? A.pin[i] : (int32_t)i) : -1;
-        }
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            const uint32_t d = (key[r] >> A.shift) & (ndig - 1);
-            const uint32_t valid = __ballot_sync(0xffffffffu, pos[r] >= 0);
-            const uint32_t peers = match_digit(d, A.digit_bits, valid);
-            const uint32_t before = hist[w * ndig + d];
-            rank[r] = before + __popc(peers & ((1u << lane) - 1));
-            __syncwarp();
-            if (pos[r] >= 0 && lane == __ffs(peers) - 1) hist[w * ndig + d] = (uint16_t)(before + __popc(peers));
-            __syncwarp();
-        }
-        __syncthreads();
-        uint32_t count = 0;
-        if (t < ndig) {
-            for (int q = 0; q < W; ++q) {
-                const uint32_t c = hist[q * ndig + t];
-                hist[q * ndig + t] = (uint16_t)count;
-                count += c;
-            }
-        }
-        __syncthreads();
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            if (pos[r] < 0) continue;
-            const uint32_t d = (key[r] >> A.shift) & (ndig - 1);
-            const int64_t o = (int64_t)base[d] + hist[w * ndig + d] + rank[r];
-            if (!MA_INB(o, 1, A.ids.n, A.ids.status)) continue;
-            A.kout[o] = key[r];
-            A.pout[o] = pos[r];
-            if (!A.kin && key[r] < (uint32_t)A.ids.rows) {
-                const uint32_t word = key[r] >> 5, bit = 1u << (key[r] & 31);
-                if (MA_INB(word, 1, A.bitmap_words, A.ids.status) &&
-                    !(*reinterpret_cast<volatile uint32_t*>(&A.bitmap[word]) & bit))
-                    atomicOr(&A.bitmap[word], bit);
-            }
-        }
-        __syncthreads();
-        if (t < ndig) base[t] += count;
-    }
-}
-
-// ------------------------------------------------------------------ sums
-
-struct SumArgs {
-    const uint32_t* keys;
-    const int32_t* pos;
-    const uint32_t* bitmap;  // NULL: no row has a token
-    const void* dy;
-    void* grad;
-    float* slots;  // per tile: the partial row of a run that began before it, and of one that goes on after it
-    int64_t n, rows, dim, ldy, ldg, slot_ld;
-    int64_t sum_blocks, zero_rows;  // blocks that sum; rows of each block after them that writes zeros
-    int32_t tile, tiles, col_blocks, accumulate;
-    float scale;
-    int* status;
-};
 
 template <bool BF16, int VEC>
 __device__ __forceinline__ void load_vec(const void* p, int64_t i, float (&f)[VEC]) {
@@ -371,9 +192,404 @@ __device__ __forceinline__ void store_vec(void* p, int64_t i, const float (&f)[V
     }
 }
 
+// One kernel's share of the rows without a token: the table is cut into parts
+// of `period` rows, a block each; rows lo .. hi - 1 of every part are this
+// kernel's. Zero is all bits zero in either type, so rows are plain bytes,
+// written in units of 16, 4 or 2.
+struct ZeroShare {
+    uint8_t* grad;
+    uint32_t* present;  // a bit per row: whether a token points to it; NULL: to none
+    int64_t rows, row_bytes, ld_bytes, period, lo, hi;
+    int32_t blocks, unit;
+    int* status;
+};
+
+__device__ __forceinline__ void write_zeros(const ZeroShare& Z, int64_t part) {
+    constexpr int G = 8;  // rows a warp looks up at once
+    const int lane = threadIdx.x & 31;
+    const int64_t r1 = min(Z.rows, part * Z.period + Z.hi);
+    for (int64_t g = part * Z.period + Z.lo + G * (threadIdx.x >> 5); g < r1; g += G * (blockDim.x >> 5)) {
+        const int64_t q = g + lane;
+        const bool empty = lane < G && q < r1 && !(Z.present && (Z.present[q >> 5] >> (q & 31) & 1u));
+        for (uint32_t todo = __ballot_sync(0xffffffffu, empty); todo; todo &= todo - 1) {
+            const int64_t r = g + __ffs(todo) - 1;
+            uint8_t* row = Z.grad + r * Z.ld_bytes;
+            if (!MA_INB(r, 1, Z.rows, Z.status)) continue;
+            if (Z.unit == 16) {
+#pragma unroll 4
+                for (int64_t c = 16 * lane; c < Z.row_bytes; c += 512)
+                    __stcs(reinterpret_cast<uint4*>(row + c), make_uint4(0, 0, 0, 0));
+            } else if (Z.unit == 4) {
+                for (int64_t c = 4 * lane; c < Z.row_bytes; c += 128) __stcs(reinterpret_cast<uint32_t*>(row + c), 0u);
+            } else {
+                for (int64_t c = 2 * lane; c < Z.row_bytes; c += 64)
+                    __stcs(reinterpret_cast<uint16_t*>(row + c), (uint16_t)0);
+            }
+        }
+    }
+}
+
+struct SortArgs {
+    Ids ids;
+    int32_t* keys;  // out: sorted keys
+    int32_t* pos;   // out: their positions
+    int32_t digit_bits, passes;
+    ZeroShare zero;  // blocks after the first find which rows of their part have tokens, and write zeros
+};
+
+// Which rows of part p have tokens, into Z.present; parts are whole words of it.
+__device__ __forceinline__ void find_present(const Ids& I, const ZeroShare& Z, int64_t p, uint32_t* bits) {
+    const int64_t r0 = p * Z.period, len = min(Z.rows - r0, Z.period);
+    const int words = (int)((len + 31) / 32);
+    for (int i = threadIdx.x; i < words; i += kSortThreads) bits[i] = 0;
+    __syncthreads();
+    for (int64_t i = threadIdx.x; i < I.n; i += 8 * kSortThreads) {
+        uint32_t key[8];
+        load_keys(I, i, kSortThreads, I.n, (uint32_t)Z.rows, key);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int64_t r = (int64_t)key[k] - r0;
+            if (r >= 0 && r < len) atomicOr(&bits[r >> 5], 1u << (r & 31));
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < words; i += kSortThreads) Z.present[r0 / 32 + i] = bits[i];
+    __syncthreads();
+}
+
+// One block sorts up to 8192 tokens, in R = ceil(n / 1024) rounds. Warp w owns
+// items 32 R w .. 32 R (w + 1) - 1, 32 a round; the rank of an item among the
+// equal digits of its warp is the warp's running count of that digit plus the
+// equal lanes before it.
+__global__ void __launch_bounds__(kSortThreads) embed_sort_small_kernel(const __grid_constant__ SortArgs A) {
+    griddep_launch_dependents();
+    griddep_wait();
+    extern __shared__ uint32_t smem[];
+    if (blockIdx.x > 0) {
+        if (A.zero.present) find_present(A.ids, A.zero, blockIdx.x - 1, smem);
+        write_zeros(A.zero, blockIdx.x - 1);
+        return;
+    }
+    uint32_t* items = smem;                                                  // 8192
+    uint16_t* hist = reinterpret_cast<uint16_t*>(smem + kSmallSort);         // [32][ndig]
+    __shared__ uint32_t warp_sums[32];
+    __shared__ uint32_t base[kMaxDigits];
+    const int t = threadIdx.x, lane = t & 31, w = t >> 5;
+    const int n = (int)A.ids.n, ndig = 1 << A.digit_bits;
+    const int rounds = (n + kSortThreads - 1) / kSortThreads;
+    const int per_warp = 32 * rounds, warps = n > 0 ? (n + per_warp - 1) / per_warp : 0;  // warps that have items
+    uint32_t item[kSortItems];
+    const int first = w * per_warp + lane;
+    load_keys(A.ids, first, 32, min(n, (w + 1) * per_warp), 0u, item);
+#pragma unroll
+    for (int r = 0; r < kSortItems; ++r) {
+        const int i = first + 32 * r;
+        item[r] = r < rounds && i < n ? (item[r] << kPosBits) | (uint32_t)i : 0xffffffffu;
+    }
+    for (int p = 0; p < A.passes; ++p) {
+        const int shift = kPosBits + p * A.digit_bits;
+        for (int i = t; i < warps * ndig / 2; i += kSortThreads) reinterpret_cast<uint32_t*>(hist)[i] = 0;
+        __syncthreads();
+        uint32_t rank[kSortItems];
+#pragma unroll
+        for (int r = 0; r < kSortItems; ++r) {
+            if (r >= rounds || w >= warps) break;
+            const uint32_t d = (item[r] >> shift) & (ndig - 1);
+            const uint32_t peers = match_digit(d, A.digit_bits, 0xffffffffu);
+            const uint32_t before = hist[w * ndig + d];
+            rank[r] = before + __popc(peers & ((1u << lane) - 1));
+            __syncwarp();
+            if (lane == __ffs(peers) - 1) hist[w * ndig + d] = (uint16_t)(before + __popc(peers));
+            __syncwarp();
+        }
+        __syncthreads();
+        uint32_t total = 0;
+        if (t < ndig) {
+#pragma unroll 8
+            for (int q = 0; q < warps; ++q) {
+                const uint32_t c = hist[q * ndig + t];
+                hist[q * ndig + t] = (uint16_t)total;
+                total += c;
+            }
+        }
+        const uint32_t excl = digit_scan<kSortThreads>(total, warp_sums);
+        if (t < ndig) base[t] = excl;
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kSortItems; ++r) {
+            if (r >= rounds || w >= warps) break;
+            const uint32_t d = (item[r] >> shift) & (ndig - 1);
+            items[base[d] + hist[w * ndig + d] + rank[r]] = item[r];
+        }
+        __syncthreads();
+        if (p + 1 < A.passes && w < warps) {
+#pragma unroll
+            for (int r = 0; r < kSortItems; ++r)
+                if (r < rounds) item[r] = items[w * per_warp + 32 * r + lane];
+        }
+    }
+    for (int i = t; i < n; i += kSortThreads) {
+        A.keys[i] = (int32_t)(items[i] >> kPosBits);
+        A.pos[i] = (int32_t)(items[i] & ((1u << kPosBits) - 1));
+    }
+}
+
+struct TileArgs {
+    Ids ids;
+    const int32_t* kin;   // NULL: the first pass, keys from the ids
+    const int32_t* pin;
+    int32_t* kout;
+    int32_t* pout;
+    uint32_t* hist;       // [digits][tiles]: tokens of a digit in a tile; after the scan, in the tiles before it
+    uint32_t* totals;     // [digits]
+    uint32_t* present;    // a bit per row, cleared by the first histogram and set by the first scatter; NULL: not needed
+    int32_t present_words;
+    ZeroShare zero;       // blocks after the sort's write zeros
+    int32_t shift, digit_bits, tiles, subtiles;  // a tile is `subtiles` runs of kTile tokens, ranked one after the other
+};
+
+// Keys of tokens first, first + stride, ... of the pass's input, `none` from `end` on.
+template <int R>
+__device__ __forceinline__ void tile_keys(const TileArgs& A, int64_t first, int64_t stride, int64_t end, uint32_t none,
+                                          uint32_t (&key)[R]) {
+    if (!A.kin) return load_keys(A.ids, first, stride, end, none, key);
+#pragma unroll
+    for (int r = 0; r < R; ++r) key[r] = first + r * stride < end ? (uint32_t)A.kin[first + r * stride] : none;
+}
+
+__global__ void __launch_bounds__(kTileThreads) embed_hist_kernel(const __grid_constant__ TileArgs A) {
+    griddep_launch_dependents();
+    griddep_wait();
+    __shared__ uint32_t h[kMaxDigits];
+    if ((int)blockIdx.x >= A.tiles) {
+        write_zeros(A.zero, blockIdx.x - A.tiles);
+        return;
+    }
+    const int ndig = 1 << A.digit_bits;
+    for (int i = threadIdx.x; i < ndig; i += kTileThreads) h[i] = 0;
+    if (!A.kin && A.present)
+        for (int i = blockIdx.x * kTileThreads + threadIdx.x; i < A.present_words; i += A.tiles * kTileThreads)
+            A.present[i] = 0;
+    __syncthreads();
+    const int64_t i0 = (int64_t)blockIdx.x * A.subtiles * kTile;
+    const int64_t i1 = min(A.ids.n, i0 + (int64_t)A.subtiles * kTile);
+    constexpr uint32_t none = 0xffffffffu;  // above every key
+    for (int64_t i = i0 + threadIdx.x; i < i1; i += kTile) {
+        uint32_t key[kTile / kTileThreads];
+        tile_keys(A, i, kTileThreads, i1, none, key);
+#pragma unroll
+        for (int k = 0; k < kTile / kTileThreads; ++k)
+            if (key[k] != none) atomicAdd(&h[(key[k] >> A.shift) & (ndig - 1)], 1u);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < ndig; i += kTileThreads) A.hist[(int64_t)i * A.tiles + blockIdx.x] = h[i];
+}
+
+// Per digit, a warp: exclusive sums over the tiles, and the total.
+__global__ void __launch_bounds__(kTileThreads) embed_scan_kernel(const __grid_constant__ TileArgs A) {
+    griddep_launch_dependents();
+    griddep_wait();
+    constexpr int W = kTileThreads / 32;
+    const int ndig = 1 << A.digit_bits, blocks = (ndig + W - 1) / W;
+    if ((int)blockIdx.x >= blocks) {
+        write_zeros(A.zero, blockIdx.x - blocks);
+        return;
+    }
+    const int d = blockIdx.x * W + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (d >= ndig) return;
+    uint32_t* h = A.hist + (int64_t)d * A.tiles;
+    uint32_t run = 0;
+    for (int q0 = 0; q0 < A.tiles; q0 += 128) {
+        uint32_t v[4], sum = 0;  // four tiles a lane, loaded side by side
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int q = q0 + 4 * lane + k;
+            v[k] = q < A.tiles ? h[q] : 0u;
+            sum += v[k];
+        }
+        uint32_t upto = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += y;
+        }
+        uint32_t before = run + upto - sum;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int q = q0 + 4 * lane + k;
+            if (q < A.tiles) h[q] = before;
+            before += v[k];
+        }
+        run += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    if (lane == 0) A.totals[d] = run;
+}
+
+constexpr int kMarkWords = 8192;  // rows of a table up to 32 times this are marked by way of shared memory
+
+__global__ void __launch_bounds__(kTileThreads) embed_scatter_kernel(const __grid_constant__ TileArgs A) {
+    griddep_launch_dependents();
+    griddep_wait();
+    constexpr int W = kTileThreads / 32, R = kTile / kTileThreads;
+    constexpr int D = (kMaxDigits + kTileThreads - 1) / kTileThreads;  // digits a thread looks after
+    extern __shared__ uint32_t marks[];  // kMarkWords, in the first pass of a table that they cover
+    __shared__ __align__(16) uint16_t hist[W * kMaxDigits];
+    __shared__ uint32_t base[kMaxDigits];
+    __shared__ uint32_t warp_sums[32];
+    if ((int)blockIdx.x >= A.tiles) {
+        write_zeros(A.zero, blockIdx.x - A.tiles);
+        return;
+    }
+    const int t = threadIdx.x, lane = t & 31, w = t >> 5;
+    const int ndig = 1 << A.digit_bits;
+    const bool mark = !A.kin && A.present, shared_marks = mark && A.present_words <= kMarkWords;
+    if (shared_marks)
+        for (int i = t; i < A.present_words; i += kTileThreads) marks[i] = 0;
+    // where this block's tokens of each digit begin: all smaller digits, and this digit in the tiles before.
+    // Thread t looks after digits D t .. D t + D - 1.
+    uint32_t own[D], sum = 0;
+#pragma unroll
+    for (int k = 0; k < D; ++k) {
+        own[k] = D * t + k < ndig ? A.totals[D * t + k] : 0u;
+        sum += own[k];
+    }
+    uint32_t excl = digit_scan<kTileThreads>(sum, warp_sums);
+#pragma unroll
+    for (int k = 0; k < D; ++k) {
+        const int d = D * t + k;
+        if (d < ndig) base[d] = excl + A.hist[(int64_t)d * A.tiles + blockIdx.x];
+        excl += own[k];
+    }
+    for (int sub = 0; sub < A.subtiles; ++sub) {
+        const int64_t i0 = ((int64_t)blockIdx.x * A.subtiles + sub) * kTile;
+        if (i0 >= A.ids.n) break;
+        for (int i = t; i < W * ndig / 2; i += kTileThreads) reinterpret_cast<uint32_t*>(hist)[i] = 0;
+        __syncthreads();
+        uint32_t key[R], rank[R];
+        int32_t pos[R];
+        const int64_t first = i0 + w * (32 * R) + lane;
+        tile_keys(A, first, 32, A.ids.n, 0u, key);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t i = first + 32 * r;
+            pos[r] = i >= A.ids.n ? -1 : A.pin ? A.pin[i] : (int32_t)i;
+        }
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const uint32_t d = (key[r] >> A.shift) & (ndig - 1);
+            const uint32_t valid = __ballot_sync(0xffffffffu, pos[r] >= 0);
+            const uint32_t peers = match_digit(d, A.digit_bits, valid);
+            const uint32_t before = hist[w * ndig + d];
+            rank[r] = before + __popc(peers & ((1u << lane) - 1));
+            __syncwarp();
+            if (pos[r] >= 0 && lane == __ffs(peers) - 1) hist[w * ndig + d] = (uint16_t)(before + __popc(peers));
+            __syncwarp();
+            if (mark && pos[r] >= 0 && key[r] < (uint32_t)A.ids.rows) {
+                const uint32_t word = key[r] >> 5, bit = 1u << (key[r] & 31);
+                if (shared_marks) atomicOr(&marks[word], bit);
+                else if (MA_INB(word, 1, A.present_words, A.ids.status) &&
+                         !(*reinterpret_cast<volatile uint32_t*>(&A.present[word]) & bit))
+                    atomicOr(&A.present[word], bit);
+            }
+        }
+        __syncthreads();
+        uint32_t count[D];
+#pragma unroll
+        for (int k = 0; k < D; ++k) {
+            const int d = D * t + k;
+            count[k] = 0;
+            if (d < ndig) {
+#pragma unroll
+                for (int q = 0; q < W; ++q) {
+                    const uint32_t c = hist[q * ndig + d];
+                    hist[q * ndig + d] = (uint16_t)count[k];
+                    count[k] += c;
+                }
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            if (pos[r] < 0) continue;
+            const uint32_t d = (key[r] >> A.shift) & (ndig - 1);
+            const int64_t o = (int64_t)base[d] + hist[w * ndig + d] + rank[r];
+            if (!MA_INB(o, 1, A.ids.n, A.ids.status)) continue;
+            A.kout[o] = (int32_t)key[r];
+            A.pout[o] = pos[r];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < D; ++k)
+            if (D * t + k < ndig) base[D * t + k] += count[k];
+    }
+    if (shared_marks) {  // one atomic per word that a tile touches, however often a token repeats in it
+        __syncthreads();
+        for (int i = t; i < A.present_words; i += kTileThreads)
+            if (marks[i]) atomicOr(&A.present[i], marks[i]);
+    }
+}
+
+// ------------------------------------------------------------------ sums
+
+struct SumArgs {
+    const int32_t* keys;
+    const int32_t* pos;
+    const void* dy;
+    void* grad;
+    float* slots;       // per tile: its part of a long run that began before it, and of one that goes on after it
+    int32_t* long_run;  // per tile: whether a long run begins in it
+    int64_t n, rows, dim, ldy, ldg, slot_ld;
+    int64_t fix_blocks;  // last kernel: blocks that add partial rows; those after them write zeros
+    ZeroShare zero;      // sums: the first blocks write zeros
+    int32_t tile, tiles, col_blocks, col_chunks, accumulate;
+    float scale;
+    int* status;
+};
+
+// A row's elements of one thread, as loaded: converted when they are added, so
+// that rows in flight take few registers.
+template <bool BF16, int VEC>
+struct Raw {
+    static constexpr int kWords = (BF16 ? (VEC + 1) / 2 : VEC);
+    uint32_t w[kWords];
+    __device__ __forceinline__ void load(const void* p, int64_t i) {
+        if constexpr (BF16) {
+            const uint16_t* q = reinterpret_cast<const uint16_t*>(p) + i;
+            if constexpr (VEC == 2) {
+                w[0] = __ldcs(reinterpret_cast<const uint32_t*>(q));
+            } else {
+                static_assert(VEC == 1);
+                w[0] = __ldcs(q);
+            }
+        } else {
+            const float* q = reinterpret_cast<const float*>(p) + i;
+            if constexpr (VEC == 2) {
+                const uint2 a = __ldcs(reinterpret_cast<const uint2*>(q));
+                w[0] = a.x; w[1] = a.y;
+            } else {
+                static_assert(VEC == 1);
+                w[0] = __float_as_uint(__ldcs(q));
+            }
+        }
+    }
+    __device__ __forceinline__ void put(int c, const uint4& v) {  // 16-byte piece c
+        w[4 * c] = v.x;
+        w[4 * c + 1] = v.y;
+        w[4 * c + 2] = v.z;
+        w[4 * c + 3] = v.w;
+    }
+    __device__ __forceinline__ void add_to(float (&acc)[VEC]) const {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+            if constexpr (BF16) acc[e] += (e & 1) ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]);
+            else acc[e] += __uint_as_float(w[e]);
+        }
+    }
+};
+
 // A finished sum: scaled, added to the old value where asked, rounded once.
 template <bool GB, int VEC>
-__device__ __forceinline__ void write_row(const SumArgs& A, uint32_t key, int64_t col, const float (&acc)[VEC]) {
+__device__ __forceinline__ void write_row(const SumArgs& A, int32_t key, int64_t col, const float (&acc)[VEC]) {
     const int64_t o = (int64_t)key * A.ldg + col;
     if (!MA_INB(o, VEC, (A.rows - 1) * A.ldg + A.dim, A.status)) return;
     float f[VEC];
@@ -388,72 +604,129 @@ __device__ __forceinline__ void write_row(const SumArgs& A, uint32_t key, int64_
     store_vec<GB, VEC>(A.grad, o, f);
 }
 
-template <bool GB, int VEC>
-__device__ __forceinline__ void zero_rows(const SumArgs& A, int64_t block) {
-    const int lane = threadIdx.x & 31;
-    const int64_t r1 = min(A.rows, (block + 1) * A.zero_rows);
-    float z[VEC];
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) z[e] = 0.f;
-    for (int64_t r = block * A.zero_rows + (threadIdx.x >> 5); r < r1; r += kSumThreads / 32) {
-        if (A.bitmap && (A.bitmap[r >> 5] >> (r & 31) & 1u)) continue;
-        for (int64_t c = VEC * lane; c < A.dim; c += VEC * 32)
-            if (MA_INB(r * A.ldg + c, VEC, (A.rows - 1) * A.ldg + A.dim, A.status))
-                store_vec<GB, VEC>(A.grad, r * A.ldg + c, z);
+// First index of sorted k[0..n) whose key is >= key.
+__device__ __forceinline__ int lower_bound(const int32_t* k, int n, int32_t key) {
+    int lo = 0, hi = n;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (k[mid] < key) lo = mid + 1;
+        else hi = mid;
     }
+    return lo;
 }
 
-constexpr int kMaxSumTile = 64;
-
 template <bool YB, bool GB, int VEC>
-__global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const __grid_constant__ SumArgs A) {
+__global__ void __launch_bounds__(kSumThreads, 4) embed_sum_kernel(const __grid_constant__ SumArgs A) {
     griddep_launch_dependents();
     griddep_wait();
-    if ((int64_t)blockIdx.x >= A.sum_blocks) {
-        zero_rows<GB, VEC>(A, blockIdx.x - A.sum_blocks);
+    constexpr int kWin = kMaxSumTile + 2 * kLong;
+    // Rows in flight: for vectors of 8, a ring of kRing 16-byte copies per thread in shared memory, four rows a
+    // step (cp.async; no thread reads another's slots, so there is no barrier); else eight rows in registers.
+    constexpr bool RING = VEC == 8;
+    constexpr int U = RING ? 4 : 8;
+    constexpr int CPY = RING ? (YB ? 1 : 2) : 1;         // 16-byte copies per row
+    constexpr int STEPS = RING ? kRing / (U * CPY) : 1;  // steps in the ring
+    extern __shared__ uint4 ring[];
+    __shared__ int32_t sk[kWin];  // keys from kLong before the tile to kLong after it, -1 and INT_MAX beyond the batch
+    __shared__ int32_t sp[kMaxSumTile + kLong];
+    if ((int)blockIdx.x < A.zero.blocks) {
+        write_zeros(A.zero, blockIdx.x);
         return;
     }
-    __shared__ uint32_t sk[kMaxSumTile + 2];  // keys, with the one before the tile and the one after it
-    __shared__ int32_t sp[kMaxSumTile];
-    const int tile = blockIdx.x / A.col_blocks;
+    const uint32_t block = blockIdx.x - A.zero.blocks;
+    const int tile = block / A.col_blocks;
     const int64_t i0 = (int64_t)tile * A.tile;
-    const int cnt = (int)min((int64_t)A.tile, A.n - i0);
-    const uint32_t none = 0xffffffffu;
-    for (int i = threadIdx.x; i < cnt + 2; i += kSumThreads) {
-        const int64_t q = i0 + i - 1;
-        sk[i] = q >= 0 && q < A.n ? A.keys[q] : none;
-        if (i >= 1 && i <= cnt) sp[i - 1] = A.pos[q];
+    int cnt = (int)min((int64_t)A.tile, A.n - i0);
+    const int win = cnt + 2 * kLong;
+    for (int q = threadIdx.x; q < win; q += blockDim.x) {
+        const int64_t i = i0 - kLong + q;
+        sk[q] = i < 0 ? -1 : i < A.n ? A.keys[i] : INT32_MAX;
+        if (q >= kLong && i < A.n) sp[q - kLong] = A.pos[i];
     }
     __syncthreads();
-    const int64_t col = ((int64_t)(blockIdx.x % A.col_blocks) * kSumThreads + threadIdx.x) * VEC;
+    const int64_t col = ((int64_t)(block % A.col_blocks) * blockDim.x + threadIdx.x) * VEC;
+    // Tokens that add to no row are last; indexes below are relative to the tile.
+    const int32_t rows = (int32_t)A.rows;
+    const int32_t* tk = sk + kLong;
+    cnt = min(cnt, lower_bound(sk, win, rows) - kLong);
+    int begin = 0, end = cnt;
+    bool head_long = false, tail_long = false;
+    if (cnt > 0) {
+        const int32_t key = tk[0];
+        if (tk[-1] == key) {  // the first run began before the tile
+            const int s = lower_bound(sk, win, key), e = lower_bound(sk, win, key + 1);
+            head_long = e - s > kLong;
+            if (!head_long) begin = min(cnt, e - kLong);  // summed where it began
+        }
+        const int32_t last = tk[cnt - 1];
+        if (tk[cnt] == last && begin < cnt && (!head_long || last != key)) {  // the last run goes on after the tile
+            const int s = lower_bound(sk, win, last), e = lower_bound(sk, win, last + 1);
+            tail_long = e - s > kLong;
+            if (!tail_long) end = e - kLong;
+        }
+    }
+    if (block % A.col_blocks == 0 && threadIdx.x == 0) A.long_run[tile] = tail_long;
     if (col >= A.dim) return;
-    bool head = sk[0] == sk[1];  // the first run began in an earlier tile
     float acc[VEC];
 #pragma unroll
     for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
-    for (int b = 0; b < cnt; b += kRowsAhead) {
-        float f[kRowsAhead][VEC];
+    bool head = head_long;
+    uint4* slots = ring + threadIdx.x;
+    auto fetch = [&](int b, int step) {  // rows b .. b + U - 1 into a step of the ring
+        if constexpr (RING) {
 #pragma unroll
-        for (int u = 0; u < kRowsAhead; ++u) {
-            if (b + u < cnt && sk[b + u + 1] < (uint32_t)A.rows) {
-                const int64_t o = (int64_t)sp[b + u] * A.ldy + col;
-                if (MA_INB(o, VEC, (A.n - 1) * A.ldy + A.dim, A.status)) load_vec<YB, VEC>(A.dy, o, f[u]);
+            for (int u = 0; u < U; ++u) {
+                if (b + u < end) {
+                    const int64_t o = (int64_t)sp[b + u] * A.ldy + col;
+                    if (MA_INB(o, VEC, (A.n - 1) * A.ldy + A.dim, A.status)) {
+                        const uint8_t* src = reinterpret_cast<const uint8_t*>(A.dy) + o * (YB ? 2 : 4);
+#pragma unroll
+                        for (int c = 0; c < CPY; ++c)
+                            cp_async16(slots + ((step * U + u) * CPY + c) * blockDim.x, src + 16 * c);
+                    }
+                }
+            }
+            cp_async_commit();  // a group per step, empty or not, so that the counts line up
+        }
+    };
+    int step = 0, ahead = 0;
+    if constexpr (RING) {
+#pragma unroll
+        for (int q = 0; q < STEPS - 1; ++q) fetch(begin + q * U, q);
+        ahead = STEPS - 1;
+    }
+    for (int b = begin; b < end; b += U) {
+        Raw<YB, VEC> f[U];
+        if constexpr (RING) {
+            fetch(b + (STEPS - 1) * U, ahead);
+            ahead = ahead + 1 == STEPS ? 0 : ahead + 1;
+            cp_async_wait<STEPS - 1>();
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int c = 0; c < CPY; ++c) f[u].put(c, slots[((step * U + u) * CPY + c) * blockDim.x]);
+            step = step + 1 == STEPS ? 0 : step + 1;
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (b + u < end) {
+                    const int64_t o = (int64_t)sp[b + u] * A.ldy + col;
+                    if (MA_INB(o, VEC, (A.n - 1) * A.ldy + A.dim, A.status)) f[u].load(A.dy, o);
+                }
             }
         }
 #pragma unroll
-        for (int u = 0; u < kRowsAhead; ++u) {
+        for (int u = 0; u < U; ++u) {
             const int i = b + u;
-            if (i >= cnt) break;
-            const uint32_t key = sk[i + 1];
-            if (key >= (uint32_t)A.rows) return;  // only tokens without a row are left
+            if (i >= end) break;
+            f[u].add_to(acc);
+            const int32_t key = tk[i];
+            if (i + 1 < end && tk[i + 1] == key) continue;
+            const bool tail = tail_long && i + 1 == end;
+            if (head || tail) {
+                float* slot = A.slots + (2 * (int64_t)tile + (head ? 0 : 1)) * A.slot_ld + col;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) acc[e] += f[u][e];
-            const bool last = i + 1 == cnt, more = sk[i + 2] == key;
-            if (!last && more) continue;
-            if (head || more) {
-                float* s = A.slots + (2 * (int64_t)tile + (head ? 0 : 1)) * A.slot_ld + col;
-#pragma unroll
-                for (int e = 0; e < VEC; ++e) s[e] = acc[e];
+                for (int e = 0; e < VEC; ++e) slot[e] = acc[e];
             } else {
                 write_row<GB, VEC>(A, key, col, acc);
             }
@@ -461,88 +734,67 @@ __global__ void __launch_bounds__(kSumThreads) embed_sum_kernel(const __grid_con
 #pragma unroll
             for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
         }
-    }
+    }    if constexpr (RING) cp_async_wait<0>();
 }
 
-// Runs that cross tiles: the partial row of the tile they begin in, then those
-// of the tiles they go on through, in that order. A block takes 32 * CV columns;
-// every warp looks at 32 tiles at a time for runs that begin in them and go
-// on. A run of up to kShortRun tiles is one warp's; of a longer one each warp
-// adds a contiguous share, and the shares are added in order.
-constexpr int kShortRun = 16;
-
-template <int CV>
-__device__ __forceinline__ void add_slots(const SumArgs& A, int64_t first, int64_t count, int64_t col,
-                                          float (&acc)[CV]) {
-#pragma unroll 4
-    for (int64_t q = 0; q < count; ++q) {
-        const float* s = A.slots + 2 * (first + q) * A.slot_ld + col;
-        float f[CV];
-        load_vec<false, CV>(s, 0, f);
-#pragma unroll
-        for (int e = 0; e < CV; ++e) acc[e] += f[e];
-    }
-}
+// The partial rows of long runs: that of the tile it begins in, then those of
+// the tiles it goes on through, in that order. A block takes 32 * CV columns
+// and the long runs that begin in kFixTiles tiles; its warps add contiguous
+// shares of a run's tiles, and the shares are added in order.
+constexpr int kFixTiles = 32;
 
 template <bool GB, int CV>
 __global__ void __launch_bounds__(kFixThreads) embed_fix_kernel(const __grid_constant__ SumArgs A) {
     griddep_launch_dependents();
     griddep_wait();
     constexpr int W = kFixThreads / 32;
-    __shared__ float part[W][32 * CV];
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int64_t col = ((int64_t)blockIdx.x * 32 + lane) * CV;
+    if ((int64_t)blockIdx.x >= A.fix_blocks) {
+        write_zeros(A.zero, blockIdx.x - A.fix_blocks);
+        return;
+    }
+    __shared__ float part[W][32 * CV];
+    const int64_t col = ((int64_t)(blockIdx.x % A.col_chunks) * 32 + lane) * CV;
     const bool in = col < A.dim;
-    for (int64_t g0 = (int64_t)blockIdx.y * 32; g0 < A.tiles; g0 += (int64_t)gridDim.y * 32) {
-        const int64_t t = g0 + lane;
-        bool starts = false;
-        if (t + 1 < A.tiles) {
-            const int64_t i1 = (t + 1) * A.tile;  // first token of the next tile
-            const uint32_t key = A.keys[i1];
-            const bool more = key < (uint32_t)A.rows && A.keys[i1 - 1] == key;
-            const bool before = t > 0 && A.keys[t * A.tile - 1] == key;  // then the whole tile is that run
-            starts = more && !before;
+    const int64_t g0 = (int64_t)(blockIdx.x / A.col_chunks) * kFixTiles;
+    uint32_t todo = __ballot_sync(0xffffffffu, g0 + lane < A.tiles && A.long_run[g0 + lane]);
+    for (; todo; todo &= todo - 1) {
+        const int64_t t0 = g0 + __ffs(todo) - 1;
+        const int32_t key = A.keys[(t0 + 1) * A.tile];
+        int64_t m = 0;  // tiles that the run goes on through
+        for (;; m += 32) {
+            const int64_t q = t0 + 1 + m + lane;
+            const uint32_t same = __ballot_sync(0xffffffffu, q < A.tiles && A.keys[q * A.tile] == key);
+            if (same != 0xffffffffu) {
+                m += __ffs(~same) - 1;
+                break;
+            }
         }
-        uint32_t todo = __ballot_sync(0xffffffffu, starts);
-        for (int k = 0; todo; todo &= todo - 1, ++k) {
-            const int64_t t0 = g0 + __ffs(todo) - 1;
-            const uint32_t key = A.keys[(t0 + 1) * A.tile];
-            int64_t m = 0;  // tiles that the run goes on through
-            for (;; m += 32) {
-                const int64_t q = t0 + 1 + m + lane;
-                const uint32_t same = __ballot_sync(0xffffffffu, q < A.tiles && A.keys[q * A.tile] == key);
-                if (same != 0xffffffffu) {
-                    m += __ffs(~same) - 1;
-                    break;
-                }
-            }
-            float acc[CV];
+        float acc[CV];
 #pragma unroll
-            for (int e = 0; e < CV; ++e) acc[e] = 0.f;
-            if (m <= kShortRun) {
-                if (k % W != w || !in) continue;
-                load_vec<false, CV>(A.slots, (2 * t0 + 1) * A.slot_ld + col, acc);
-                add_slots<CV>(A, t0 + 1, m, col, acc);
-                write_row<GB, CV>(A, key, col, acc);
-                continue;
-            }
-            const int64_t lo = m * w / W, hi = m * (w + 1) / W;
-            if (in) {
-                if (w == 0) load_vec<false, CV>(A.slots, (2 * t0 + 1) * A.slot_ld + col, acc);
-                add_slots<CV>(A, t0 + 1 + lo, hi - lo, col, acc);
+        for (int e = 0; e < CV; ++e) acc[e] = 0.f;
+        if (in) {
+            if (w == 0) load_vec<false, CV>(A.slots, (2 * t0 + 1) * A.slot_ld + col, acc);
+            const int64_t hi = m * (w + 1) / W;
+#pragma unroll 8
+            for (int64_t q = m * w / W; q < hi; ++q) {
+                float f[CV];
+                load_vec<false, CV>(A.slots, 2 * (t0 + 1 + q) * A.slot_ld + col, f);
 #pragma unroll
-                for (int e = 0; e < CV; ++e) part[w][lane * CV + e] = acc[e];
+                for (int e = 0; e < CV; ++e) acc[e] += f[e];
             }
-            __syncthreads();
-            if (w == 0 && in) {
 #pragma unroll
-                for (int q = 1; q < W; ++q)
-#pragma unroll
-                    for (int e = 0; e < CV; ++e) acc[e] += part[q][lane * CV + e];
-                write_row<GB, CV>(A, key, col, acc);
-            }
-            __syncthreads();
+            for (int e = 0; e < CV; ++e) part[w][lane * CV + e] = acc[e];
         }
+        __syncthreads();
+        if (w == 0 && in) {
+#pragma unroll
+            for (int q = 1; q < W; ++q)
+#pragma unroll
+                for (int e = 0; e < CV; ++e) acc[e] += part[q][lane * CV + e];
+            write_row<GB, CV>(A, key, col, acc);
+        }
+        __syncthreads();
     }
 }
 
@@ -559,36 +811,52 @@ struct LookupArgs {
 
 constexpr int kLookupThreads = 256;
 
-template <bool TB, bool OB, int VEC>
-__global__ void __launch_bounds__(kLookupThreads) embed_lookup_kernel(const __grid_constant__ LookupArgs A) {
+template <bool TB, bool OB, int VEC, int TOKENS>
+__global__ void __launch_bounds__(kLookupThreads, 4) embed_lookup_kernel(const __grid_constant__ LookupArgs A) {
     griddep_launch_dependents();
     griddep_wait();
-    const int lanes = 1 << A.lanes_log2;
-    const int64_t i = ((int64_t)blockIdx.x << (8 - A.lanes_log2)) + (threadIdx.x >> A.lanes_log2);
-    if (i >= A.ids.n || !MA_INB(i, 1, A.ids.n, A.ids.status)) return;
-    const int64_t id =
-        A.ids.i64 ? reinterpret_cast<const int64_t*>(A.ids.p)[i] : reinterpret_cast<const int32_t*>(A.ids.p)[i];
-    const bool in = id >= 0 && id < A.ids.rows;
-    const int t = threadIdx.x & (lanes - 1);
-    if (!in && id != A.ids.padding && t == 0) record_error(A.ids.status, MA_ERR_BOUNDS);
-    constexpr int U = 4;
+    const int lanes = 1 << A.lanes_log2, t = threadIdx.x & (lanes - 1);
+    const int groups = kLookupThreads >> A.lanes_log2;
+    // this thread's rows: T of them, `groups` apart; their ids before anything depends on one
+    constexpr int T = TOKENS, U = 4 / TOKENS;
+    const int64_t i0 = (int64_t)blockIdx.x * groups * T + (threadIdx.x >> A.lanes_log2);
+    int64_t id[T];
+    bool in[T], real[T];
+#pragma unroll
+    for (int k = 0; k < T; ++k) {
+        const int64_t i = i0 + k * groups;
+        real[k] = i < A.ids.n && MA_INB(i, 1, A.ids.n, A.ids.status);
+        id[k] = !real[k]    ? 0
+                : A.ids.i64 ? reinterpret_cast<const int64_t*>(A.ids.p)[i]
+                            : reinterpret_cast<const int32_t*>(A.ids.p)[i];
+    }
+#pragma unroll
+    for (int k = 0; k < T; ++k) {
+        in[k] = real[k] && id[k] >= 0 && id[k] < A.ids.rows;
+        if (real[k] && !in[k] && id[k] != A.ids.padding && t == 0) record_error(A.ids.status, MA_ERR_BOUNDS);
+    }
     for (int64_t c0 = (int64_t)t * VEC; c0 < A.dim; c0 += (int64_t)U * lanes * VEC) {
-        float f[U][VEC];
+        float f[T][U][VEC];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t c = c0 + (int64_t)u * lanes * VEC;
-            if (in && c < A.dim && MA_INB(id * A.ldt + c, VEC, (A.ids.rows - 1) * A.ldt + A.dim, A.ids.status))
-                load_vec<TB, VEC>(A.table, id * A.ldt + c, f[u]);
-        }
+        for (int k = 0; k < T; ++k)
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t c = c0 + (int64_t)u * lanes * VEC;
-            if (c >= A.dim) break;
+            for (int u = 0; u < U; ++u) {
+                const int64_t c = c0 + (int64_t)u * lanes * VEC;
+                if (in[k] && c < A.dim &&
+                    MA_INB(id[k] * A.ldt + c, VEC, (A.ids.rows - 1) * A.ldt + A.dim, A.ids.status))
+                    load_vec<TB, VEC>(A.table, id[k] * A.ldt + c, f[k][u]);
+            }
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) f[u][e] = in ? f[u][e] * A.scale : 0.f;
-            if (MA_INB(i * A.ldo + c, VEC, (A.ids.n - 1) * A.ldo + A.dim, A.ids.status))
-                store_vec<OB, VEC>(A.out, i * A.ldo + c, f[u]);
-        }
+        for (int k = 0; k < T; ++k)
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t c = c0 + (int64_t)u * lanes * VEC, i = i0 + k * groups;
+                if (!real[k] || c >= A.dim) continue;
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) f[k][u][e] = in[k] ? f[k][u][e] * A.scale : 0.f;
+                if (MA_INB(i * A.ldo + c, VEC, (A.ids.n - 1) * A.ldo + A.dim, A.ids.status))
+                    store_vec<OB, VEC>(A.out, i * A.ldo + c, f[k][u]);
+            }
     }
 }
 
@@ -610,17 +878,17 @@ struct GradLayout {
     bool small;
     int digit_bits, passes, tiles, subtiles;
     int sum_tile;  // tokens per tile of the sum
-    int64_t bitmap_words, sum_tiles, slot_ld;
-    size_t off_k0, off_p0, off_k1, off_p1, off_hist, off_bitmap, off_slots, total;
+    int64_t sum_tiles, slot_ld;
+    size_t off_k0, off_p0, off_k1, off_p1, off_hist, off_present, off_long, off_slots, total;
 };
 
 // Tokens per tile of the sum: the longest of 64, 32, 16 and 8 that still gives
-// about four blocks to each of 148 SMs (a longer tile leaves fewer partial
-// rows; too few blocks leave SMs without loads in flight).
+// six blocks of 256 threads to each of 148 SMs (a longer tile searches less
+// and leaves fewer partial rows; too few blocks leave SMs without loads in flight).
 int sum_tile(int64_t n, int64_t dim) {
     const int64_t col_blocks = (dim + 8 * kSumThreads - 1) / (8 * kSumThreads);
     int s = kMaxSumTile;
-    while (s > 8 && (n + s - 1) / s * col_blocks < 4 * 148) s /= 2;
+    while (s > 8 && (n + s - 1) / s * col_blocks < 6 * 148) s /= 2;
     return s;
 }
 
@@ -628,14 +896,13 @@ GradLayout grad_layout(int64_t n, int64_t rows, int64_t dim) {
     GradLayout L;
     std::memset(&L, 0, sizeof(L));
     const int bits = bits_for(rows);
-    L.small = n <= kSmallSort && bits <= kSmallKeyBits;
+    L.small = n == 0 || (n <= kSmallSort && bits <= kSmallKeyBits);
     L.passes = (bits + kMaxDigitBits - 1) / kMaxDigitBits;
     L.digit_bits = (bits + L.passes - 1) / L.passes;
     L.tiles = (int)((n + kTile - 1) / kTile);
     L.subtiles = (L.tiles + kMaxTiles - 1) / kMaxTiles;
     if (L.subtiles > 1) L.tiles = (L.tiles + L.subtiles - 1) / L.subtiles;
     L.subtiles = std::max(1, L.subtiles);
-    L.bitmap_words = (rows + 31) / 32;
     L.slot_ld = (dim + 7) / 8 * 8;
     L.sum_tile = sum_tile(n, dim);
     L.sum_tiles = (n + L.sum_tile - 1) / L.sum_tile;
@@ -649,8 +916,9 @@ GradLayout grad_layout(int64_t n, int64_t rows, int64_t dim) {
     L.off_p0 = take((size_t)n * 4);
     L.off_k1 = take(L.small ? 0 : (size_t)n * 4);
     L.off_p1 = take(L.small ? 0 : (size_t)n * 4);
-    L.off_hist = take(L.small ? 0 : (size_t)L.tiles * kMaxDigits * 4);
-    L.off_bitmap = take((size_t)L.bitmap_words * 4);
+    L.off_hist = take(L.small ? 0 : (size_t)(L.tiles + 1) * kMaxDigits * 4);  // the totals after the tiles
+    L.off_present = take(((size_t)rows + 31) / 32 * 4);
+    L.off_long = take((size_t)L.sum_tiles * 4);
     L.off_slots = take((size_t)L.sum_tiles * 2 * L.slot_ld * 4);
     L.total = off;
     return L;
@@ -658,34 +926,102 @@ GradLayout grad_layout(int64_t n, int64_t rows, int64_t dim) {
 
 constexpr size_t kSmallSortSmem = (size_t)kSmallSort * 4 + 32 * kMaxDigits * 2;
 
-cudaError_t sort_small_setup() {
+cudaError_t launch_sort_small(const SortArgs& A, unsigned grid, cudaStream_t s) {
     static PerDevice<int> cache;
     int dev = 0, done = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    return cache.get(dev, &done, [](int* v) {
+    e = cache.get(dev, &done, [](int* v) {
         *v = 1;
         return cudaFuncSetAttribute(embed_sort_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     (int)kSmallSortSmem);
     });
+    if (e != cudaSuccess) return e;
+    return launch_pdl(embed_sort_small_kernel, dim3(grid), dim3(kSortThreads), kSmallSortSmem, s, A);
 }
 
 template <bool YB, bool GB, int VEC>
-cudaError_t launch_sum(const SumArgs& A, unsigned grid, cudaStream_t s) {
-    return launch_pdl(embed_sum_kernel<YB, GB, VEC>, dim3(grid), dim3(kSumThreads), 0, s, A);
+cudaError_t launch_sum(const SumArgs& A, unsigned grid, unsigned threads, cudaStream_t s) {
+    const size_t ring = VEC == 8 ? (size_t)threads * kRing * 16 : 0;
+    static PerDevice<int> cache;
+    int dev = 0, done = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    e = cache.get(dev, &done, [](int* v) {
+        *v = 1;
+        return cudaFuncSetAttribute(embed_sum_kernel<YB, GB, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kSumThreads * kRing * 16);
+    });
+    if (e != cudaSuccess) return e;
+    return launch_pdl(embed_sum_kernel<YB, GB, VEC>, dim3(grid), dim3(threads), ring, s, A);
 }
 
-template <bool YB, bool GB>
-cudaError_t launch_sum_vec(const SumArgs& A, int vec, unsigned grid, cudaStream_t s) {
-    return vec == 8   ? launch_sum<YB, GB, 8>(A, grid, s)
-           : vec == 2 ? launch_sum<YB, GB, 2>(A, grid, s)
-                      : launch_sum<YB, GB, 1>(A, grid, s);
+// The parts of the zeros that the kernels write, in order: while the tokens are
+// sorted, beside the sums, and beside the last kernel. Sort and last kernel
+// last about as long as HBM takes for kSortHides and kLastHides bytes (small
+// batches: the whole sort; by tiles: what comes after the first scatter).
+struct ZeroPlan {
+    ZeroShare z;
+    int64_t cut[4];  // rows of each part: [cut[0], cut[1]) by the first kernels, ...
+    ZeroShare part(int k) const {
+        ZeroShare s = z;
+        s.lo = cut[k];
+        s.hi = cut[k + 1];
+        if (s.hi <= s.lo) s.blocks = 0;
+        return s;
+    }
+    ZeroShare part(int k, int of, int i) const {  // slice i of `of` of part k
+        ZeroShare s = part(k);
+        const int64_t len = cut[k + 1] - cut[k];
+        s.lo = cut[k] + len * i / of;
+        s.hi = cut[k] + len * (i + 1) / of;
+        if (s.hi <= s.lo) s.blocks = 0;
+        return s;
+    }
+};
+constexpr double kSortHides = 60e6, kLastHides = 30e6;
+
+ZeroPlan plan_zeros(void* grad, int64_t rows, int64_t dim, int64_t ldg, int gsz, uint32_t* present, bool none, int sms) {
+    ZeroPlan P;
+    std::memset(&P, 0, sizeof(P));
+    ZeroShare& z = P.z;
+    z.grad = reinterpret_cast<uint8_t*>(grad);
+    z.present = present;
+    z.rows = rows;
+    z.row_bytes = dim * gsz;
+    z.ld_bytes = ldg * gsz;
+    z.status = device_status_ptr();
+    if (none) return P;
+    const uint64_t bits = reinterpret_cast<uintptr_t>(grad) | (uint64_t)z.row_bytes | (uint64_t)z.ld_bytes;
+    z.unit = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
+    // two parts per SM, in whole words of the bit map, no more rows than the one-block sort's kernel has bits for
+    z.period = ((rows + 2 * sms - 1) / (2 * sms) + 31) / 32 * 32;
+    z.period = std::min<int64_t>(z.period, (int64_t)kSmallSortSmem * 8);
+    z.blocks = (int32_t)((rows + z.period - 1) / z.period);
+    const double bytes = (double)rows * z.row_bytes;
+    const int64_t first = (int64_t)std::min((double)z.period, std::ceil(z.period * kSortHides / bytes));
+    const int64_t last = (int64_t)std::min((double)(z.period - first), std::ceil(z.period * kLastHides / bytes));
+    P.cut[0] = 0;
+    P.cut[1] = first;
+    P.cut[2] = z.period - last;
+    P.cut[3] = z.period;
+    return P;
 }
 
-cudaError_t run_sum(const SumArgs& A, int ydt, int gdt, int vec, unsigned grid, cudaStream_t s) {
-    if (ydt == MA_BF16)
-        return gdt == MA_BF16 ? launch_sum_vec<true, true>(A, vec, grid, s) : launch_sum_vec<true, false>(A, vec, grid, s);
-    return gdt == MA_BF16 ? launch_sum_vec<false, true>(A, vec, grid, s) : launch_sum_vec<false, false>(A, vec, grid, s);
+// f(vector width as a constant) for rows that take vectors of 8, 2 or 1 elements
+template <typename F>
+cudaError_t with_vec(int vec, F f) {
+    return vec == 8   ? f(std::integral_constant<int, 8>{})
+           : vec == 2 ? f(std::integral_constant<int, 2>{})
+                      : f(std::integral_constant<int, 1>{});
+}
+// f(constants: whether each of two types is bf16)
+template <typename F>
+cudaError_t with_types(int a, int b, F f) {
+    using T = std::true_type;
+    using N = std::false_type;
+    if (a == MA_BF16) return b == MA_BF16 ? f(T{}, T{}) : f(T{}, N{});
+    return b == MA_BF16 ? f(N{}, T{}) : f(N{}, N{});
 }
 
 int cuda_rc(cudaError_t e) { return e == cudaSuccess ? MA_OK : MA_ERR_CUDA; }
@@ -742,21 +1078,21 @@ int lookup(int64_t n, const void* ids, int idt, int64_t rows, int64_t dim, const
     for (int v : {8, 2})
         if (vec == 1 && rows_take(table, dim, ldt, tsz, v) && rows_take(out, dim, ldo, osz, v)) vec = v;
     while (A.lanes_log2 < 8 && ((int64_t)vec << A.lanes_log2) < dim) ++A.lanes_log2;
-    const int64_t per_block = int64_t(1) << (8 - A.lanes_log2);
+    // Two tokens a thread where a row takes at most two vectors of each of its threads and the batch fills the GPU
+    // either way: four loads in flight per thread instead of two.
+    const bool two = dim <= ((int64_t)2 * vec << A.lanes_log2) && (n << A.lanes_log2) >= (int64_t)2048 * 148;
+    const int64_t per_block = (int64_t)(two ? 2 : 1) << (8 - A.lanes_log2);
     const dim3 grid((unsigned)((n + per_block - 1) / per_block)), block(kLookupThreads);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int pr = prof_begin(MA_PROF_EMBED, s);
-    auto go = [&](auto v) -> cudaError_t {
-        constexpr int V = decltype(v)::value;
-        if (tdt == MA_BF16)
-            return odt == MA_BF16 ? launch_pdl(embed_lookup_kernel<true, true, V>, grid, block, 0, s, A)
-                                  : launch_pdl(embed_lookup_kernel<true, false, V>, grid, block, 0, s, A);
-        return odt == MA_BF16 ? launch_pdl(embed_lookup_kernel<false, true, V>, grid, block, 0, s, A)
-                              : launch_pdl(embed_lookup_kernel<false, false, V>, grid, block, 0, s, A);
-    };
-    const cudaError_t e = vec == 8   ? go(std::integral_constant<int, 8>{})
-                          : vec == 2 ? go(std::integral_constant<int, 2>{})
-                                     : go(std::integral_constant<int, 1>{});
+    const cudaError_t e = with_vec(vec, [&](auto v) {
+        return with_types(tdt, odt, [&](auto tb, auto ob) {
+            constexpr bool TB = decltype(tb)::value, OB = decltype(ob)::value;
+            constexpr int V = decltype(v)::value;
+            return two ? launch_pdl(embed_lookup_kernel<TB, OB, V, 2>, grid, block, 0, s, A)
+                       : launch_pdl(embed_lookup_kernel<TB, OB, V, 1>, grid, block, 0, s, A);
+        });
+    });
     prof_end(pr, s, 0.0, (double)n * dim * (tsz + osz));
     return cuda_rc(e);
 }
@@ -781,12 +1117,15 @@ int grad(int64_t n, const void* ids, int idt, int64_t rows, int64_t dim, const v
     uint8_t* base = reinterpret_cast<uint8_t*>(ws);
     auto at32 = [&](size_t off) { return reinterpret_cast<uint32_t*>(base + off); };
     const Ids I{ids, n, rows, padding, idt == MA_I64, device_status_ptr()};
+    auto at_i = [&](size_t off) { return reinterpret_cast<int32_t*>(base + off); };
+    const int ysz = ydt == MA_BF16 ? 2 : 4, gsz = gdt == MA_BF16 ? 2 : 4;
+    int vec = 1;
+    for (int v : {8, 2})
+        if (vec == 1 && rows_take(dY, dim, ldy, ysz, v) && rows_take(g, dim, ldg, gsz, v)) vec = v;
     SumArgs S;
     std::memset(&S, 0, sizeof(S));
-    S.bitmap = n > 0 ? at32(L.off_bitmap) : nullptr;
     S.dy = dY;
     S.grad = g;
-    S.slots = n > 0 ? reinterpret_cast<float*>(base + L.off_slots) : nullptr;
     S.n = n;
     S.rows = rows;
     S.dim = dim;
@@ -796,69 +1135,94 @@ int grad(int64_t n, const void* ids, int idt, int64_t rows, int64_t dim, const v
     S.scale = scale;
     S.accumulate = accumulate;
     S.status = device_status_ptr();
-    const int ysz = ydt == MA_BF16 ? 2 : 4, gsz = gdt == MA_BF16 ? 2 : 4;
-    int vec = 1;
-    for (int v : {8, 2})
-        if (vec == 1 && rows_take(dY, dim, ldy, ysz, v) && rows_take(g, dim, ldg, gsz, v)) vec = v;
-    S.col_blocks = (int)((dim + kSumThreads * vec - 1) / (kSumThreads * vec));
     S.tile = L.sum_tile;
     S.tiles = (int)L.sum_tiles;
-    S.sum_blocks = (int64_t)S.tiles * S.col_blocks;
-    // a block that writes zeros covers about 64 KB of rows
-    S.zero_rows = std::max<int64_t>(4, (int64_t(1) << 16) / (dim * gsz) / 4 * 4);
-    const int64_t blocks = S.sum_blocks + (accumulate ? 0 : (rows + S.zero_rows - 1) / S.zero_rows);
-    if (blocks > INT32_MAX) return MA_ERR_UNSUPPORTED;
-    const uint32_t* keys = nullptr;
-    const int32_t* pos = nullptr;
+    // a thread takes one vector of a row: as few blocks of up to 256 threads across the columns as hold them all
+    const int64_t vecs = (dim + vec - 1) / vec;
+    S.col_blocks = (int)((vecs + kSumThreads - 1) / kSumThreads);
+    const unsigned threads = (unsigned)((vecs + S.col_blocks - 1) / S.col_blocks + 31) / 32 * 32;
+    const int cv = std::min(vec, 4);
+    S.col_chunks = (int)((dim + 32 * cv - 1) / (32 * cv));
+    const int64_t sum_blocks = (int64_t)S.tiles * S.col_blocks;
+    S.fix_blocks = S.tiles > 1 ? (int64_t)((S.tiles + kFixTiles - 1) / kFixTiles) * S.col_chunks : 0;
+    uint32_t* present = n > 0 ? at32(L.off_present) : nullptr;
+    const ZeroPlan zeros = plan_zeros(g, rows, dim, ldg, gsz, present, accumulate != 0, sms);
+    if ((int64_t)S.tiles * S.col_blocks + zeros.z.blocks > INT32_MAX || S.fix_blocks + zeros.z.blocks > INT32_MAX)
+        return MA_ERR_UNSUPPORTED;
+    if (n > 0) {
+        S.slots = reinterpret_cast<float*>(base + L.off_slots);
+        S.long_run = at_i(L.off_long);
+    }
     const int pr = prof_begin(MA_PROF_EMBED, s);
     cudaError_t e = cudaSuccess;
-    if (n > 0 && L.small) {
-        if ((e = sort_small_setup()) != cudaSuccess) return MA_ERR_CUDA;
-        SortArgs A{I, at32(L.off_k0), reinterpret_cast<int32_t*>(base + L.off_p0), at32(L.off_bitmap),
-                   (int32_t)L.bitmap_words, L.digit_bits, L.passes};
-        e = launch_pdl(embed_sort_small_kernel, dim3(1), dim3(kSortThreads), kSmallSortSmem, s, A);
-        keys = A.keys;
-        pos = A.pos;
-    } else if (n > 0) {
+    if (L.small) {
+        SortArgs A;
+        std::memset(&A, 0, sizeof(A));
+        A.ids = I;
+        A.keys = at_i(L.off_k0);
+        A.pos = at_i(L.off_p0);
+        A.digit_bits = L.digit_bits;
+        A.passes = L.passes;
+        A.zero = zeros.part(0);
+        if (n == 0) A.zero.hi = zeros.z.period;  // nothing else runs
+        else A.zero.blocks = zeros.z.blocks;     // every part's rows are looked at, whatever its share
+        e = launch_sort_small(A, (unsigned)(A.zero.blocks + 1), s);
+        S.keys = A.keys;
+        S.pos = A.pos;
+    } else {
         TileArgs A;
         std::memset(&A, 0, sizeof(A));
         A.ids = I;
         A.hist = at32(L.off_hist);
-        A.bitmap = at32(L.off_bitmap);
-        A.bitmap_words = (int32_t)L.bitmap_words;
+        A.totals = A.hist + (size_t)L.tiles * kMaxDigits;
+        A.present = accumulate ? nullptr : present;
+        A.present_words = (int32_t)((rows + 31) / 32);
+        const int scan_blocks = ((1 << L.digit_bits) + kTileThreads / 32 - 1) / (kTileThreads / 32);
         A.digit_bits = L.digit_bits;
         A.tiles = L.tiles;
         A.subtiles = L.subtiles;
+        const int after = 3 * (L.passes - 1);  // launches after the first scatter: a share of the zeros beside each
+        auto share = [&](int launch) {
+            if (launch >= 3) A.zero = zeros.part(0, after, launch - 3);
+            return A.zero.blocks;
+        };
         for (int p = 0; p < L.passes && e == cudaSuccess; ++p) {
             const bool odd = p & 1;
-            A.kout = at32(odd ? L.off_k1 : L.off_k0);
-            A.pout = reinterpret_cast<int32_t*>(base + (odd ? L.off_p1 : L.off_p0));
+            A.kout = at_i(odd ? L.off_k1 : L.off_k0);
+            A.pout = at_i(odd ? L.off_p1 : L.off_p0);
             A.shift = p * L.digit_bits;
-            e = launch_pdl(embed_hist_kernel, dim3(L.tiles), dim3(kTileThreads), 0, s, A);
-            if (e == cudaSuccess) e = launch_pdl(embed_scatter_kernel, dim3(L.tiles), dim3(kTileThreads), 0, s, A);
+            const dim3 threads(kTileThreads);
+            const int z0 = share(3 * p);
+            e = launch_pdl(embed_hist_kernel, dim3(L.tiles + z0), threads, 0, s, A);
+            const int z1 = share(3 * p + 1);
+            if (e == cudaSuccess) e = launch_pdl(embed_scan_kernel, dim3(scan_blocks + z1), threads, 0, s, A);
+            const int z2 = share(3 * p + 2);
+            const size_t marks = p == 0 && A.present && A.present_words <= kMarkWords ? A.present_words * 4 : 0;
+            if (e == cudaSuccess) e = launch_pdl(embed_scatter_kernel, dim3(L.tiles + z2), threads, marks, s, A);
             A.kin = A.kout;
             A.pin = A.pout;
         }
-        keys = A.kin;
-        pos = A.pin;
+        S.keys = A.kin;
+        S.pos = A.pin;
     }
-    if (e != cudaSuccess) return MA_ERR_CUDA;
-    S.keys = keys;
-    S.pos = pos;
-    e = run_sum(S, ydt, gdt, vec, (unsigned)blocks, s);
-    if (e == cudaSuccess && S.tiles > 1) {
-        const int cv = vec == 1 ? 1 : vec == 2 ? 2 : 4;
-        auto fix = [&](auto v) -> cudaError_t {
-            constexpr int V = decltype(v)::value;
-            const unsigned gx = (unsigned)((dim + 32 * V - 1) / (32 * V));
-            const unsigned gy =
-                (unsigned)std::max<int64_t>(1, std::min<int64_t>((S.tiles + 31) / 32, 8 * (int64_t)sms / gx));
-            return gdt == MA_BF16 ? launch_pdl(embed_fix_kernel<true, V>, dim3(gx, gy), dim3(kFixThreads), 0, s, S)
-                                  : launch_pdl(embed_fix_kernel<false, V>, dim3(gx, gy), dim3(kFixThreads), 0, s, S);
-        };
-        e = cv == 1   ? fix(std::integral_constant<int, 1>{})
-            : cv == 2 ? fix(std::integral_constant<int, 2>{})
-                      : fix(std::integral_constant<int, 4>{});
+    if (e == cudaSuccess && n > 0) {
+        S.zero = zeros.part(1);
+        // a table of one digit is sorted by its first pass: no launch was left to hide zeros beside
+        if (!L.small && L.passes == 1) S.zero.lo = 0, S.zero.blocks = zeros.z.blocks;
+        const unsigned grid = (unsigned)(S.zero.blocks + S.tiles * S.col_blocks);
+        e = with_vec(vec, [&](auto v) {
+            return with_types(ydt, gdt, [&](auto yb, auto gb) {
+                return launch_sum<decltype(yb)::value, decltype(gb)::value, decltype(v)::value>(S, grid, threads, s);
+            });
+        });
+        S.zero = zeros.part(2);
+        if (e == cudaSuccess && S.fix_blocks + S.zero.blocks > 0)
+            e = with_vec(vec, [&](auto v) {
+                constexpr int CV = decltype(v)::value < 4 ? decltype(v)::value : 4;
+                const dim3 g2((unsigned)(S.fix_blocks + S.zero.blocks)), b2(kFixThreads);
+                return gdt == MA_BF16 ? launch_pdl(embed_fix_kernel<true, CV>, g2, b2, 0, s, S)
+                                      : launch_pdl(embed_fix_kernel<false, CV>, g2, b2, 0, s, S);
+            });
     }
     prof_end(pr, s, 0.0, (double)n * dim * ysz + (double)rows * dim * gsz);
     return cuda_rc(e);

@@ -131,6 +131,9 @@ def test_nothing_to_do():
     ma.embedding_grad(none, torch.zeros((0, 8), device="cuda"), grad)
     assert not grad.any()
     ma.embedding_grad(none, torch.zeros((0, 0), device="cuda"), torch.zeros((10, 0), device="cuda"))
+    large = torch.ones((1 << 20, 3), dtype=torch.bfloat16, device="cuda")
+    ma.embedding_grad(none, torch.zeros((0, 3), device="cuda"), large)
+    assert not large.any()
     assert ma.embedding_lookup(none, grad).shape == (0, 8)
     assert ma.embedding_lookup(none + 0, torch.zeros((0, 8), device="cuda")).shape == (0, 8)
 
@@ -258,6 +261,23 @@ def test_streams_and_captured_replay():
         check_grad(grad, *ref_grad(ids, dy, V, 1.0))
         assert torch.equal(out, grad[ids])
     assert ma.ma_device_status() == ma.MA_OK
+
+
+def test_runs_around_the_lengths_where_they_are_cut():
+    # runs of 1 to 400 tokens, beginning at every offset of a tile, some after one another without a gap
+    r = np.random.default_rng(3)
+    lengths = [1, 63, 64, 65, 127, 128, 129, 130, 191, 192, 193, 255, 256, 257, 400] + list(r.integers(1, 300, 120))
+    for n_extra in (0, 9000):  # the one-block sort takes the first, the sort by tiles both together
+        V, D = 700, 24
+        runs = r.permutation(lengths)[:40 if not n_extra else None]
+        keys = np.repeat(np.sort(r.permutation(V)[:len(runs)]), runs)
+        ids = torch.from_numpy(r.permutation(keys).astype(np.int64)).cuda()
+        assert (len(keys) > 8192) == bool(n_extra)
+        dy = torch.randn((len(keys), D), generator=gen(9), device="cuda")
+        grad = torch.full((V, D), 7.0, device="cuda")
+        ma.embedding_grad(ids, dy, grad)
+        check_grad(grad, *ref_grad(ids, dy, V, 1.0))
+        assert ma.ma_device_status() == ma.MA_OK
 
 
 def test_many_tokens_reach_several_tiles_per_block():
