@@ -8,6 +8,7 @@ the C names (``ma_partition``, ``muon_step_batched``, ``adamw_step_fused``,
 """
 from __future__ import annotations
 
+import array
 import contextlib
 import ctypes
 import math
@@ -202,10 +203,12 @@ def _ptr(x) -> int:
 
 def _ptr_array(xs) -> ctypes.Array:
     try:
-        ptrs = [x.data_ptr() for x in xs]
-    except AttributeError:  # plain addresses, or None, among them
-        ptrs = [_ptr(x) for x in xs]
-    return (ctypes.c_void_p * max(1, len(ptrs)))(*ptrs)
+        ptrs = array.array("Q", map(_torch().Tensor.data_ptr, xs))
+    except TypeError:  # plain addresses, or None, among them
+        ptrs = array.array("Q", map(_ptr, xs))
+    if not ptrs:
+        ptrs.append(0)
+    return (ctypes.c_void_p * len(ptrs)).from_buffer(ptrs)
 
 
 _TORCH = None
@@ -378,8 +381,8 @@ def adamw_step_fused(P, G, M, V, hp: AdamWHParams, stream=None, gdt: int | None 
     if gdt is None:
         gdt = _dtype_code(G[0]) if n else MA_F32
     if numel is None:
-        numel = [p.numel() for p in P]
-    nar = (ctypes.c_int64 * max(1, n))(*numel)
+        numel = map(_torch().Tensor.numel, P)
+    nar = (ctypes.c_int64 * max(1, n)).from_buffer(array.array("q", numel) or array.array("q", [0]))
     _check(lib().adamw_step_fused_clipped(n, _ptr_array(P), _ptr_array(G), int(gdt), _ptr_array(M), _ptr_array(V),
                                           nar, ctypes.byref(hp), _ptr(clip), _stream(stream)), "adamw_step_fused")
 

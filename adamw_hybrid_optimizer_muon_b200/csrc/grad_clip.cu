@@ -21,7 +21,7 @@
 //    with what the norm pass left in L2. Norm and scaling of the 1.12 GB depth-20
 //    set take 518 us, 167 of them the norm (the persistent ring for both: 567).
 //  * Small sets, one launch in all (below): the 81 gains and scalars of the
-//    depth-20 set take 5.6 us in place, with three launches 9.5.
+//    depth-20 set take 5.1 us in place, with three launches 9.5.
 //
 // The squares are summed in fp32 over the 32 or 64 values a thread holds of one
 // chunk (relative error at most 64 * 2^-24 of a sum of positive terms, in
@@ -52,6 +52,7 @@ constexpr int kBlocksPerSm = 2;
 constexpr int kAhead = 3;                             // chunks in flight per block
 constexpr int kRingBytes = kAhead * kThreads * kVecs * 16;  // 96 KB
 constexpr int kSmallTable = 96;                       // tensors of the small parameter block (2.4 KB)
+constexpr int kMidTable = 640;                        // tensors of a small set's larger one (15 KB)
 
 // A gradient: its first 16-byte word at or before the data, and how many
 // leading elements of that word belong to something else, so that every
@@ -62,8 +63,7 @@ struct GradDesc {
     int64_t chunk0_skip;  // first chunk of this tensor * 8 + leading elements to skip (0..7)
 };
 
-// Small sets (up to kSmallChunks chunks of 2 KB, one table of kSmallTable
-// tensors) take one launch of one cluster: every warp sums its chunks, the
+// Small sets (small_chunks() chunks of 2 KB) take one launch of one cluster: every warp sums its chunks, the
 // cluster adds its blocks' sums through distributed shared memory, and clipping
 // reads the chunks again, from L2. Latency is all there: one launch in place of
 // two or three, few dependent loads, and little code to fetch.
@@ -72,7 +72,14 @@ constexpr int64_t kSmallChunkVecs = 32 * kSmallVecs;   // words per chunk (2 KB)
 constexpr int kSmallBlocks = 8;                        // blocks of the cluster
 constexpr int kSmallThreads = 1024;
 constexpr int kSmallWarps = kSmallBlocks * kSmallThreads / 32;
-constexpr int kSmallChunks = 4 * kSmallWarps;
+// A set whose table fits the 2.4 KB block is small while each warp has one
+// chunk (512 KB: clipped in 5.2 us, by the streaming kernels in 7.4; at 1 MB 9.3
+// against 7.4); one with more tensors, whose other way is the 31 KB table in
+// three launches, up to four chunks a warp (600 tensors of 100 values: 8.9
+// against 10.6 us; of 800 values: 10.4 against 10.6).
+constexpr int small_chunks(size_t tensors) {
+    return tensors <= kSmallTable ? kSmallWarps : tensors <= kMidTable ? 4 * kSmallWarps : 0;
+}
 
 template <int CAP>
 struct GradTable {
@@ -443,9 +450,9 @@ cudaError_t clip_setup() {
     });
 }
 
-template <bool CLIP>
+template <int CAP, bool CLIP>
 __global__ void __cluster_dims__(kSmallBlocks, 1, 1) __launch_bounds__(kSmallThreads)
-    grad_small_kernel(const __grid_constant__ GradTable<kSmallTable> T) {
+    grad_small_kernel(const __grid_constant__ GradTable<CAP> T) {
     griddep_launch_dependents();
     static_assert(kSmallThreads == 1024, "one partial sum per lane of the first warp");
     __shared__ double red[kSmallThreads / 32];
@@ -454,8 +461,9 @@ __global__ void __cluster_dims__(kSmallBlocks, 1, 1) __launch_bounds__(kSmallThr
     const int lane = threadIdx.x & 31, rank = (int)cluster_ctarank();
     const int first = rank * (kSmallThreads / 32) + (threadIdx.x >> 5);
     const GradDesc* tab = table(T);
-    auto find = [&](int64_t c) {  // kSmallTable tensors: three loads a lane, side by side
-        int count = 0;
+    auto find = [&](int64_t c) {
+        if constexpr (CAP > kSmallTable) return tab[search_tensor(tab, T.n, c)];
+        int count = 0;  // three loads a lane, side by side
 #pragma unroll
         for (int b = 0; b < kSmallTable; b += 32)
             count += __popc(__ballot_sync(0xffffffffu, b + lane < T.n && chunk0_of(tab[b + lane]) <= c));
@@ -586,31 +594,36 @@ cudaError_t launch_table(const std::vector<GradItem>& items, size_t first, size_
                     : launch_pdl(grad_sumsq_kernel<CAP>, grid, dim3(kThreads), kRingBytes, s, T);
 }
 
+template <int CAP>
 cudaError_t launch_small(const std::vector<GradItem>& items, bool in_place, const ClipArgs& a, cudaStream_t s) {
-    static thread_local GradTable<kSmallTable> T;
+    static thread_local GradTable<CAP> T;
     fill_table(T, items, 0, items.size(), kSmallChunkVecs, 0, false, a);
-    return in_place ? launch_pdl(grad_small_kernel<true>, dim3(kSmallBlocks), dim3(kSmallThreads), 0, s, T)
-                    : launch_pdl(grad_small_kernel<false>, dim3(kSmallBlocks), dim3(kSmallThreads), 0, s, T);
+    return in_place ? launch_pdl(grad_small_kernel<CAP, true>, dim3(kSmallBlocks), dim3(kSmallThreads), 0, s, T)
+                    : launch_pdl(grad_small_kernel<CAP, false>, dim3(kSmallBlocks), dim3(kSmallThreads), 0, s, T);
 }
 
 }  // namespace
 
+template <int CAP>
+bool is_small(const void* func) {
+    return func == reinterpret_cast<const void*>(grad_small_kernel<CAP, false>);
+}
+
 size_t clip_patch_bytes(const void* func) {
     if (func == reinterpret_cast<const void*>(clip_finalize_kernel)) return sizeof(ClipFinalize);
-    if (func == reinterpret_cast<const void*>(grad_small_kernel<false>)) return sizeof(GradTable<kSmallTable>);
+    if (is_small<kSmallTable>(func)) return sizeof(GradTable<kSmallTable>);
+    if (is_small<kMidTable>(func)) return sizeof(GradTable<kMidTable>);
     return 0;
 }
 
 void clip_patch(const void* func, void* arg, float scale, float max_norm) {
-    if (func == reinterpret_cast<const void*>(clip_finalize_kernel)) {
-        ClipFinalize* F = reinterpret_cast<ClipFinalize*>(arg);
-        F->scale = scale;
-        F->max_norm = max_norm;
-    } else {
-        GradTable<kSmallTable>* T = reinterpret_cast<GradTable<kSmallTable>*>(arg);
-        T->scale = scale;
-        T->max_norm = max_norm;
-    }
+    auto set = [&](auto* p) {
+        p->scale = scale;
+        p->max_norm = max_norm;
+    };
+    if (is_small<kSmallTable>(func)) set(reinterpret_cast<GradTable<kSmallTable>*>(arg));
+    else if (is_small<kMidTable>(func)) set(reinterpret_cast<GradTable<kMidTable>*>(arg));
+    else set(reinterpret_cast<ClipFinalize*>(arg));
 }
 
 cudaError_t launch_clip_finalize(const ClipArgs& a, int nparts, cudaStream_t s) {
@@ -637,15 +650,16 @@ cudaError_t launch_grad_clip(const std::vector<GradItem>& items, const ClipArgs&
         ++*launches;
         return launch_clip_finalize(a, 0, s);
     }
-    if (items.size() <= kSmallTable) {
+    if (items.size() <= kMidTable) {
         int64_t chunks = 0, bytes = 0;
         for (const GradItem& it : items) {
             chunks += chunks_of(it, kSmallChunkVecs);
             bytes += it.numel * (it.gdt == MA_BF16 ? 2 : 4);
         }
-        if (chunks <= kSmallChunks) {
+        if (chunks <= small_chunks(items.size())) {
             const int pr = prof_begin(MA_PROF_CLIP, s);
-            const cudaError_t e = launch_small(items, in_place, a, s);
+            const cudaError_t e = items.size() <= kSmallTable ? launch_small<kSmallTable>(items, in_place, a, s)
+                                                              : launch_small<kMidTable>(items, in_place, a, s);
             prof_end(pr, s, 0.0, (double)bytes * (in_place ? 2 : 1));
             ++*launches;
             return e;
@@ -724,7 +738,7 @@ int grad_clip(int n, const void* const* G, const int32_t* gdt, const int64_t* nu
         items.push_back({G[i], numel[i], gdt[i]});
     }
     if (in_place) {
-        std::sort(w.begin(), w.end());
+        if (!std::is_sorted(w.begin(), w.end())) std::sort(w.begin(), w.end());
         for (size_t k = 1; k < w.size(); ++k)
             if (w[k].first < w[k - 1].second) return MA_ERR_ARG;
     }

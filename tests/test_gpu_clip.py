@@ -31,6 +31,12 @@ LISTS = {
     "chunk edges": [(16384, "bf16", 0), (16385, "bf16", 0), (16383, "bf16", 0), (8192, "fp32", 0), (8193, "fp32", 3),
                     (16384, "bf16", 7), (16377, "bf16", 7), (2 * 16384 + 1, "bf16", 1)],
     "97 tensors": [(100 + 7 * k, "bf16" if k % 2 else "fp32", k % 4) for k in range(97)],
+    "640 tensors": [(1 + k % 70, "bf16" if k % 3 else "fp32", k % 4) for k in range(640)],
+    "641 tensors": [(1 + k % 70, "bf16" if k % 3 else "fp32", k % 4) for k in range(641)],
+    "256 small chunks": [(128 * 4 * 100, "fp32", 0), (128 * 8 * 156, "bf16", 0)],
+    "257 small chunks": [(128 * 4 * 100 + 1, "fp32", 0), (128 * 8 * 156, "bf16", 0)],
+    "1024 small chunks": [(512, "fp32", 0)] * 99 + [(128 * 8 * 925, "bf16", 0)],
+    "1025 small chunks": [(512, "fp32", 0)] * 99 + [(128 * 8 * 925 + 1, "bf16", 0)],
     "1281 tensors": [(1 + k % 50, "bf16" if k % 3 else "fp32", k % 4) for k in range(1281)],
     "3000 tensors, some long": [(40000 if k % 500 == 0 else 1 + k % 9, "bf16", 0) for k in range(3000)],
     "long": [(9_000_001, "bf16", 1), (4_000_003, "fp32", 0)],
