@@ -493,11 +493,18 @@ def _on_stream(stream):
     return torch.cuda.stream(s)
 
 
+def _new(like, shape, dtype, stream):
+    """An uninitialised tensor on ``like``'s device, allocated for ``stream``."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    with _on_stream(stream):
+        return like.new_empty(shape, dtype=dtype)
+
+
 def embedding_lookup(ids, table, scale: float = 1.0, padding: int | None = None, out=None, dtype=None, stream=None):
     """Rows of an embedding table by token: out[...] = scale * table[ids[...]], rounded once to ``dtype`` (fp32 or
     bf16; default: the table's), or into ``out`` (shape ids.shape + (dim,)). An id outside the table gives zeros and
     records MA_ERR_BOUNDS in the status word, except ``padding`` (-1, say), which only gives zeros."""
-    torch = _torch()
     _on_current_gpu("embedding_lookup", ids, table, out)
     ids, idt = _ids(ids, stream)
     if table.dim() != 2:
@@ -505,8 +512,7 @@ def embedding_lookup(ids, table, scale: float = 1.0, padding: int | None = None,
     V, D = table.shape
     tab, ldt = _rows(table, "embedding_lookup: table")
     if out is None:
-        with _on_stream(stream):
-            out = torch.empty(ids.shape + (D,), dtype=dtype or table.dtype, device=table.device)
+        out = _new(table, (*ids.shape, D), dtype or table.dtype, stream)
     elif out.shape != ids.shape + (D,) or (dtype is not None and out.dtype != dtype):
         raise MAError(MA_ERR_SHAPE, "embedding_lookup: out has another shape or dtype")
     rows, ldo = _rows(out, "embedding_lookup: out")
@@ -531,7 +537,6 @@ def embedding_grad(ids, grad_rows, grad, scale: float = 1.0, padding: int | None
     reads) is written, zeros where no token points; with ``accumulate`` the sums are added to the rows that have
     tokens. fp32 sums in token order, no atomics: the same inputs give the same bits. Tokens equal to ``padding``
     add nothing. ws: workspace (embed_grad_workspace_bytes; allocated here when None). Returns ``grad``."""
-    torch = _torch()
     _on_current_gpu("embedding_grad", ids, grad_rows, grad, ws)
     ids, idt = _ids(ids, stream)
     if grad.dim() != 2 or grad_rows.shape != ids.shape + (grad.shape[1],):
@@ -539,15 +544,16 @@ def embedding_grad(ids, grad_rows, grad, scale: float = 1.0, padding: int | None
     V, D = grad.shape
     g, ldg = _rows(grad, "embedding_grad: grad")
     y, ldy = _rows(grad_rows, "embedding_grad: grad_rows")
-    need = embed_grad_workspace_bytes(ids.numel(), V, D)
-    if ws is None and need:
-        with _on_stream(stream):
-            ws = torch.empty(need, dtype=torch.uint8, device=grad.device)
-    _check(lib().ma_embed_grad(ids.numel(), _ptr(ids), idt, V, D, _ptr(y), _dtype_code(grad_rows), ldy, float(scale),
+    n = ids.numel()
+    if ws is None:
+        ws_bytes = embed_grad_workspace_bytes(n, V, D)
+        if ws_bytes:
+            ws = _new(grad, ws_bytes, _torch().uint8, stream)
+    else:
+        ws_bytes = ws.numel() * ws.element_size()
+    _check(lib().ma_embed_grad(n, _ptr(ids), idt, V, D, _ptr(y), _dtype_code(grad_rows), ldy, float(scale),
                                NO_PADDING if padding is None else int(padding), int(bool(accumulate)), _ptr(g),
-                               _dtype_code(grad), ldg, _ptr(ws),
-                               ws.numel() * ws.element_size() if ws is not None else 0, _stream(stream)),
-           "embedding_grad")
+                               _dtype_code(grad), ldg, _ptr(ws), ws_bytes, _stream(stream)), "embedding_grad")
     return grad
 
 
@@ -613,7 +619,7 @@ def qk_max_logit(q, k, scale: float | None = None, causal: bool = True, offsets=
     nd = 3 if offsets is not None else 4
     if q.dim() != nd or k.dim() != nd or q.shape[:-2] != k.shape[:-2] or q.shape[-1] != k.shape[-1]:
         raise MAError(MA_ERR_SHAPE, "qk_max_logit: q and k must be (sequences x) tokens x heads x dim")
-    if q.dtype != torch.bfloat16 or k.dtype != torch.bfloat16:
+    if q.dtype is not torch.bfloat16 or k.dtype is not torch.bfloat16:
         raise MAError(MA_ERR_DTYPE, "qk_max_logit: q and k must be bf16")
     qt, kt = q.stride(), k.stride()
     H, KV, D = q.shape[-2], k.shape[-2], q.shape[-1]
@@ -622,8 +628,7 @@ def qk_max_logit(q, k, scale: float | None = None, causal: bool = True, offsets=
     if accumulate and out is None:
         raise MAError(MA_ERR_NULL, "qk_max_logit: accumulate needs out")
     if out is None:
-        with _on_stream(stream):
-            out = torch.empty(H, dtype=torch.float32, device=q.device)
+        out = _new(q, H, torch.float32, stream)
     elif out.shape != (H,) or out.dtype != torch.float32 or not out.is_contiguous():
         raise MAError(MA_ERR_SHAPE, "qk_max_logit: out must be heads contiguous fp32 values")
     if offsets is not None:

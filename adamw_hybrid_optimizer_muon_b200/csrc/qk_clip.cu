@@ -787,30 +787,29 @@ int qk_max(int64_t seqs, int64_t len, int64_t total, int heads, int kv_heads, in
     if (reinterpret_cast<uintptr_t>(out) % 4 != 0 || reinterpret_cast<uintptr_t>(offsets) % 4 != 0) return MA_ERR_ALIGN;
     const int64_t tokens = offsets ? total : len, outer = offsets ? 1 : seqs;
     const bool work = seqs > 0 && len > 0 && tokens > 0;
+    int64_t st[6] = {q_tok, q_head, q_seq, k_tok, k_head, k_seq};
     if (work) {
         if (!q || !k) return MA_ERR_NULL;
         if (dim % 8 != 0 || reinterpret_cast<uintptr_t>(q) % 16 != 0 || reinterpret_cast<uintptr_t>(k) % 16 != 0)
             return MA_ERR_ALIGN;
-        const int64_t st[6] = {q_tok, q_head, q_seq, k_tok, k_head, k_seq};
         const int64_t ext[6] = {tokens, heads, outer, tokens, kv_heads, outer};
         for (int i = 0; i < 6; ++i) {
-            if (st[i] < 0 || (ext[i] > 1 && st[i] < dim)) return MA_ERR_SHAPE;
+            if (ext[i] == 1) st[i] = dim;  // never followed
+            if (st[i] < dim) return MA_ERR_SHAPE;
             if (st[i] % 8 != 0) return MA_ERR_ALIGN;
             if (st[i] >= (int64_t(1) << 38)) return MA_ERR_UNSUPPORTED;
         }
     }
-    int sms = 0, st;
-    if ((st = device_ready(&sms))) return st;
+    int sms = 0;
+    if (const int rc = device_ready(&sms)) return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     QkLaunch L;
     std::memset(&L, 0, sizeof(L));
     const int n = tile_keys(dim);
     const int chunks = (dim + kBK - 1) / kBK;
     if (work) {
-        // a stride of an extent of 1 is never followed, but the map wants one of at least 16 bytes
-        auto fix = [&](int64_t x) { return x > 0 ? x : (int64_t)8 * ((dim + 7) / 8); };
-        if (!make_map(&L.mq, q, dim, tokens, heads, outer, fix(q_tok), fix(q_head), fix(q_seq), kRows) ||
-            !make_map(&L.mk, k, dim, tokens, kv_heads, outer, fix(k_tok), fix(k_head), fix(k_seq), n))
+        if (!make_map(&L.mq, q, dim, tokens, heads, outer, st[0], st[1], st[2], kRows) ||
+            !make_map(&L.mk, k, dim, tokens, kv_heads, outer, st[3], st[4], st[5], n))
             return MA_ERR_CUDA;
     }
     const int pr = prof_begin(MA_PROF_QK, s);

@@ -183,6 +183,12 @@ def test_views_of_a_fused_projection(KV):
     assert torch.equal(got, ma.qk_max_logit(qh.transpose(1, 2), kh.transpose(1, 2)))
 
 
+def test_strides_of_extents_of_one_are_not_looked_at():
+    q, k = randn((1, 200, 1, 64), 30), randn((1, 200, 1, 64), 31)
+    odd = lambda x: x.as_strided(x.shape, (3, 64, 5, 1))  # noqa: E731  one sequence, one head
+    assert torch.equal(ma.qk_max_logit(q, k), ma.qk_max_logit(odd(q), odd(k)))
+
+
 def test_micro_batches_add_up():
     q, k = randn((6, 200, 2, 128), 6), randn((6, 200, 2, 128), 7)
     whole = ma.qk_max_logit(q, k)
