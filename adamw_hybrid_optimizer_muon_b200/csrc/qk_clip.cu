@@ -17,13 +17,23 @@
 // blocks of 128 rows, in shared memory, and streams tiles of N keys past them,
 // 64 columns of the head dimension a stage; both blocks multiply a key tile
 // before it is released, which halves the key traffic from L2, and while one
-// block's accumulator is reduced the other's is computed.
+// block's accumulator is reduced (480 cycles) the other's is computed (1024
+// for 128 x 256 x 128).
 //
 // Work is counted in (128 queries x N keys) products, of which causality and the
 // sequences' ends leave only those with a visible pair. A maximum can be cut
 // anywhere, so the CTAs take equal shares of that count, wherever it falls in a
 // head or a sequence, with no scheduler and no second pass: each segment ends
 // in one atomic maximum per warp (order does not change a maximum).
+//
+// 4096 tokens x 32 heads x 128, causal: 48 us, 1.44 PFLOP/s of the visible pairs
+// (6 % more are computed in the diagonal tiles), 61 us at the 1.54 GHz that the
+// power cap leaves in a long run. About 1250 cycles a product of 1024; what is
+// left is the issuing warp's own time between products and the shared memory
+// that MMA operands (96 bytes a clock) and arriving keys (32) share. Under 1024
+// tokens a head the latency of start and end, about 5 us, counts. CTA pairs
+// (256-row blocks, half the keys loaded by each CTA) were slower, 58 us: each
+// product then waits for an arrival from the other CTA.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -45,9 +55,13 @@ constexpr uint32_t kSmemMax = 232448;          // 227 KB
 constexpr uint32_t kCtlBytes = 512;
 constexpr int kMaxChunks = 4;                  // head dimension up to 256
 constexpr int kMaxStages = 12;
-// Stages of N keys x 64 columns that fit beside two blocks of queries of CH chunks.
+// Buffers for blocks of queries: where the shared memory allows, a third one, so
+// that the next segment's first block arrives while this one's are in use.
+constexpr int q_buffers(int ch) { return ch <= 2 ? 3 : 2; }
+// Stages of N keys x 64 columns that fit beside them.
 constexpr int stages(int n, int ch) {
-    const int fit = (int)((kSmemMax - 1024 - kCtlBytes - 2 * ch * kQChunk) / (uint32_t)(n * kBK * 2));
+    const int fit =
+        (int)((kSmemMax - 1024 - kCtlBytes - q_buffers(ch) * ch * kQChunk) / (uint32_t)(n * kBK * 2));
     return fit < kMaxStages ? fit : kMaxStages;
 }
 constexpr long long kDrainNs = 50000000LL;  // bound of the waits for this CTA's own copies and MMAs at its end
@@ -95,7 +109,7 @@ struct QkLaunch {
 
 struct QkCtl {
     uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t q_full[2], q_empty[2];
+    uint64_t q_full[3], q_empty[3];
     uint64_t acc_full[4], acc_empty[4];
     uint64_t drain;
     uint32_t tmem_base;
@@ -225,10 +239,9 @@ struct Walk {
 };
 
 // The loading and the MMA warp run their loops with all lanes together, every
-// value the same in each, and one elected lane issues. (Issued from inside a
-// one-lane branch, each MMA cost about 140 cycles of issue, more than its own
-// 128 x 256 x 16 product takes: operands of these instructions live in uniform
-// registers, which code for one lane of a divergent warp has to fill each time.)
+// value the same in each, and one elected lane issues. Issued from inside a
+// one-lane branch, with the work between two products spread over branches, the
+// same products took 70 us in place of 48.
 
 // 4-D tiled load global -> shared, completing on `bar`, after announcing its bytes there.
 __device__ __forceinline__ void load_4d(uint32_t smem_dst, const CUtensorMap* map, uint32_t bar, int c0, int c1, int c2,
@@ -400,9 +413,9 @@ __global__ void __launch_bounds__(kThreads, 1) qk_max_kernel(const __grid_consta
     constexpr int NB = 512 / N / 2;  // accumulators per block of rows
     extern __shared__ __align__(16) uint8_t raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) / 1024 * 1024);
-    constexpr int nst = stages(N, CH);
-    uint8_t* qbuf = smem;  // [block of rows][chunk]
-    uint8_t* ring = qbuf + 2 * CH * kQChunk;
+    constexpr int nst = stages(N, CH), NQ = q_buffers(CH);
+    uint8_t* qbuf = smem;  // [buffer][chunk]
+    uint8_t* ring = qbuf + NQ * CH * kQChunk;
     QkCtl* ctl = reinterpret_cast<QkCtl*>(ring + nst * kStage);
     const int warp = uniform(threadIdx.x >> 5), lane = threadIdx.x & 31;
     const Waits W{&ctl->abort_flag, L.wait_limit_ns, L.status};
@@ -412,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) qk_max_kernel(const __grid_consta
             mbar_init(&ctl->full[s], 1);
             mbar_init(&ctl->empty[s], 1);
         }
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < NQ; ++s) {
             mbar_init(&ctl->q_full[s], 1);
             mbar_init(&ctl->q_empty[s], 1);
         }
@@ -445,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1) qk_max_kernel(const __grid_consta
     const uint32_t q_full_bar = smem_u32(&ctl->q_full[0]), q_empty_bar = smem_u32(&ctl->q_empty[0]);
     const uint32_t acc_full_bar = smem_u32(&ctl->acc_full[0]), acc_empty_bar = smem_u32(&ctl->acc_empty[0]);
     if (warp == 0) {
-        int stage = 0, uses = 0, q_uses0 = 0, q_uses1 = 0;
+        int stage = 0, uses = 0, loads = 0;  // loads: blocks of queries so far, each into the next buffer
         uint32_t phase = 0;
         bool ok = true;
         Walk<N, CAUSAL> walk(L, ctl);
@@ -453,13 +466,14 @@ __global__ void __launch_bounds__(kThreads, 1) qk_max_kernel(const __grid_consta
         while (ok && walk.next(g)) {
             g.make_uniform();
             const int kvh = g.h / (L.heads / L.kv);
-            auto load_q = [&](int s, int& n) {
-                if (!wait(q_empty_bar + 8 * s, (n & 1u) ^ 1u, W)) return false;
-                ++n;
-                expect_bytes(q_full_bar + 8 * s, CH * kQChunk);
+            auto load_q = [&](int s) {
+                const int n = loads / NQ, at = loads - n * NQ;
+                if (!wait(q_empty_bar + 8 * at, (n & 1u) ^ 1u, W)) return false;
+                ++loads;
+                expect_bytes(q_full_bar + 8 * at, CH * kQChunk);
 #pragma unroll
                 for (int c = 0; c < CH; ++c)
-                    load_4d(q_base + (s * CH + c) * kQChunk, &L.mq, q_full_bar + 8 * s, c * kBK,
+                    load_4d(q_base + (at * CH + c) * kQChunk, &L.mq, q_full_bar + 8 * at, c * kBK,
                             g.tok0 + g.q0 + s * kRows, g.h, g.b);
                 return true;
             };
@@ -467,8 +481,8 @@ __global__ void __launch_bounds__(kThreads, 1) qk_max_kernel(const __grid_consta
             for (int j = g.first(); j < end && ok; ++j) {
                 // in the order the MMAs take them: lower queries, keys, upper queries
                 const bool in0 = g.in0(j), q1 = g.in1(j) && j == g.a1;
-                if (in0 && j == g.a0) ok = load_q(0, q_uses0);
-                if (ok && !in0 && q1) ok = load_q(1, q_uses1);
+                if (in0 && j == g.a0) ok = load_q(0);
+                if (ok && !in0 && q1) ok = load_q(1);
 #pragma unroll
                 for (int c = 0; c < CH; ++c) {
                     if (!ok || !(ok = wait(empty_bar + 8 * stage, phase ^ 1u, W))) break;
@@ -480,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) qk_max_kernel(const __grid_consta
                         phase ^= 1u;
                     }
                 }
-                if (ok && in0 && q1) ok = load_q(1, q_uses1);
+                if (ok && in0 && q1) ok = load_q(1);
             }
         }
         // every copy of this CTA has landed before it exits (an abort leaves some unread)
@@ -488,30 +502,36 @@ __global__ void __launch_bounds__(kThreads, 1) qk_max_kernel(const __grid_consta
             const int n = uses / nst + (s < uses % nst ? 1 : 0);  // uses of stage s
             if (n > 0) wait_on(full_bar + 8 * s, (n - 1) & 1u, W, kDrainNs, true);
         }
-        if (q_uses0 > 0) wait_on(q_full_bar, (q_uses0 - 1) & 1u, W, kDrainNs, true);
-        if (q_uses1 > 0) wait_on(q_full_bar + 8, (q_uses1 - 1) & 1u, W, kDrainNs, true);
+        for (int s = 0; s < NQ; ++s) {
+            const int n = loads / NQ + (s < loads % NQ ? 1 : 0);
+            if (n > 0) wait_on(q_full_bar + 8 * s, (n - 1) & 1u, W, kDrainNs, true);
+        }
     } else if (warp == 1) {
         // The MMA queue is a few products deep: what this warp does between the products of one block of rows
         // and the next has to fit in the time of about three of them.
         constexpr uint32_t IDESC = idesc_bf16_f32(kRows, N, 0);
         const uint64_t desc = smem_desc_sw128(0, 16, 1024);  // plus an address in 16-byte units
         const uint64_t qd = desc + (q_base >> 4);
-        int stage = 0, q_uses0 = 0, q_uses1 = 0, acc0 = 0, acc1 = 0;  // uses of each block's queries, accumulators
+        int stage = 0, loads = 0, acc0 = 0, acc1 = 0;  // blocks of queries so far; uses of each block's accumulators
+        int q0 = 0, q1 = 0;                            // the buffers that hold them
         uint32_t phase = 0;
         bool ok = true;
         Walk<N, CAUSAL> walk(L, ctl);
         Segment g;
         // the products of block S with the key tile at the ring's stage; `first`: its copies are waited for,
         // `last`: its stages are released
-        auto block = [&](auto which, int& uses, int& q_uses, bool fresh, bool first, bool last, bool done) {
+        auto block = [&](auto which, int& uses, int& at, bool fresh, bool first, bool last, bool done) {
             constexpr int S = decltype(which)::value;
             const int a = S * NB + (NB == 1 ? 0 : uses & (NB - 1));
             if (!wait(acc_empty_bar + 8 * a, ((uses / NB) & 1u) ^ 1u, W)) return false;
             ++uses;
             if (fresh) {
-                if (!wait(q_full_bar + 8 * S, q_uses & 1u, W)) return false;
-                ++q_uses;
+                const int n = loads / NQ;
+                at = loads - n * NQ;
+                if (!wait(q_full_bar + 8 * at, n & 1u, W)) return false;
+                ++loads;
             }
+            const uint64_t q = qd + ((uint32_t)(at * CH * kQChunk) >> 4);
             const uint32_t d = tmem + (uint32_t)(a * N);
             int st = stage;
             uint32_t ph = phase;
@@ -522,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) qk_max_kernel(const __grid_consta
                     if (!wait(full_bar + 8 * st, ph, W)) return false;
                     tc_fence_after();
                 }
-                const uint64_t ad = qd + (((S * CH + c) * kQChunk) >> 4), bd = desc + ((ring_base + st * kStage) >> 4);
+                const uint64_t ad = q + ((c * kQChunk) >> 4), bd = desc + ((ring_base + st * kStage) >> 4);
                 if (c == 0) mma_f16<false>(d, ad, bd, IDESC);
                 else mma_f16<true>(d, ad, bd, IDESC);
 #pragma unroll
@@ -538,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) qk_max_kernel(const __grid_consta
                 phase = ph;
             }
             commit(acc_full_bar + 8 * a);
-            if (done) commit(q_empty_bar + 8 * S);
+            if (done) commit(q_empty_bar + 8 * at);
             return true;
         };
         while (ok && walk.next(g)) {
@@ -547,9 +567,9 @@ __global__ void __launch_bounds__(kThreads, 1) qk_max_kernel(const __grid_consta
             for (int j = g.first(); j < end && ok; ++j) {
                 const bool in0 = g.in0(j), in1 = g.in1(j);
                 if (in0)
-                    ok = block(std::integral_constant<int, 0>{}, acc0, q_uses0, j == g.a0, true, !in1, j + 1 == g.b0);
+                    ok = block(std::integral_constant<int, 0>{}, acc0, q0, j == g.a0, true, !in1, j + 1 == g.b0);
                 if (ok && in1)
-                    ok = block(std::integral_constant<int, 1>{}, acc1, q_uses1, j == g.a1, !in0, true, j + 1 == g.b1);
+                    ok = block(std::integral_constant<int, 1>{}, acc1, q1, j == g.a1, !in0, true, j + 1 == g.b1);
             }
         }
         commit(smem_u32(&ctl->drain));  // every MMA has read its operands before this CTA exits
@@ -743,7 +763,7 @@ bool make_map(CUtensorMap* map, const void* base, int64_t dim, int64_t tokens, i
 template <int N, int CH, bool CAUSAL, bool ABS>
 cudaError_t launch_max(const QkLaunch& L, int grid, cudaStream_t s) {
     static_assert(stages(N, CH) >= CH, "a key tile has to fit in the ring");
-    constexpr uint32_t smem = 1024 + 2 * CH * kQChunk + stages(N, CH) * N * kBK * 2 + kCtlBytes;
+    constexpr uint32_t smem = 1024 + q_buffers(CH) * CH * kQChunk + stages(N, CH) * N * kBK * 2 + kCtlBytes;
     static PerDevice<int> cache;
     int dev = 0, done = 0;
     cudaError_t e = cudaGetDevice(&dev);
