@@ -7,14 +7,19 @@
 // The gradient reads each row of dY once and writes each row of the table's
 // gradient once: the tokens are sorted (stably, by radix), equal tokens stand
 // next to each other, and their rows are added in registers, in token order.
-// No atomics touch a value, so the same inputs give the same bits, and a token
-// that fills the batch costs what any other batch does.
+// No atomics touch a value, so the same inputs give the same bits. A token that
+// fills the batch costs up to 1.4 times what distinct tokens do (131,072 x 1280
+// bf16 into 65,536 rows: 161 us, 116 us for uniform tokens, whose rows all go
+// from the sums straight to the table).
 //
 // Sort. Keys are token ids; positions of the batch travel with them. Up to
 // 8192 tokens of a table of fewer than 2^19 rows are sorted by one block in
 // shared memory, key and position packed into 32 bits; more by tiles of 1024, a
 // histogram, a scan and a scatter launch per digit. Digits have up to nine bits:
-// a vocabulary below 2^18 takes two passes.
+// a vocabulary below 2^18 takes two passes. A whole gradient of 32,000 x 128
+// bf16 by the one block (by the tiles): 100 tokens 12.4 us (26.9), 2048 15.0
+// (31.2), 8192 25.9 (33.2); the one block's time grows with the tokens, and 8192
+// keys and their digit counts are what its shared memory is laid out for.
 //
 // Sum. The sorted tokens are cut into tiles of S. A block takes one tile and a
 // range of columns and adds up the runs of equal tokens that begin in its tile,
@@ -28,6 +33,12 @@
 // HBM idle, so the zeros are spread: each kernel from the one that knows which
 // rows have tokens on (a bit per row) writes a share beside its own work, the
 // sums the rest.
+//
+// Measured, bf16: 8192 tokens x 4096 into 32,000 rows 75 us, of which the 262 MB
+// written take 61 at the 4.3 TB/s that plain stores reach on this GPU; 131,072 x
+// 1280 of a skewed distribution into 65,536 rows 138 us for 503 MB. Rows that are
+// not whole 16-byte vectors go by two elements or by one, and issue bounds them:
+// uniform tokens of 1282 columns 189 us and of 1281 columns 309, of 1280 118.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -53,7 +64,7 @@ constexpr int kTile = kTileThreads * 8;  // tokens a block ranks at a time
 constexpr int kMaxTiles = 4096;          // tiles of a pass; longer batches have longer tiles
 constexpr int kSumThreads = 256;         // at most
 constexpr int kFixThreads = 256;
-constexpr int kMaxSumTile = 64;
+constexpr int kMaxSumTile = 512;
 constexpr int kRing = 16;                // 16-byte copies in flight per thread of the sums
 constexpr int kLong = 32;                // tokens; a longer run is cut at the tiles' borders
 
@@ -194,13 +205,12 @@ __device__ __forceinline__ void store_vec(void* p, int64_t i, const float (&f)[V
 
 // One kernel's share of the rows without a token: the table is cut into parts
 // of `period` rows, a block each; rows lo .. hi - 1 of every part are this
-// kernel's. Zero is all bits zero in either type, so rows are plain bytes,
-// written in units of 16, 4 or 2.
+// kernel's. Zero is all bits zero in either type, so rows are plain bytes.
 struct ZeroShare {
     uint8_t* grad;
     uint32_t* present;  // a bit per row: whether a token points to it; NULL: to none
     int64_t rows, row_bytes, ld_bytes, period, lo, hi;
-    int32_t blocks, unit;
+    int32_t blocks, aligned;  // aligned: every row begins and ends at a 16-byte boundary
     int* status;
 };
 
@@ -215,16 +225,17 @@ __device__ __forceinline__ void write_zeros(const ZeroShare& Z, int64_t part) {
             const int64_t r = g + __ffs(todo) - 1;
             uint8_t* row = Z.grad + r * Z.ld_bytes;
             if (!MA_INB(r, 1, Z.rows, Z.status)) continue;
-            if (Z.unit == 16) {
-#pragma unroll 4
-                for (int64_t c = 16 * lane; c < Z.row_bytes; c += 512)
-                    __stcs(reinterpret_cast<uint4*>(row + c), make_uint4(0, 0, 0, 0));
-            } else if (Z.unit == 4) {
-                for (int64_t c = 4 * lane; c < Z.row_bytes; c += 128) __stcs(reinterpret_cast<uint32_t*>(row + c), 0u);
-            } else {
-                for (int64_t c = 2 * lane; c < Z.row_bytes; c += 64)
-                    __stcs(reinterpret_cast<uint16_t*>(row + c), (uint16_t)0);
+            // 2-byte units up to the first 16-byte boundary (at most seven), 16-byte units, 2-byte units (at most seven)
+            int64_t head = 0, body = Z.row_bytes;
+            if (!Z.aligned) {
+                head = min(Z.row_bytes, (int64_t)(-reinterpret_cast<intptr_t>(row) & 15));
+                body = head + (Z.row_bytes - head) / 16 * 16;
+                if (2 * lane < head) __stcs(reinterpret_cast<uint16_t*>(row) + lane, (uint16_t)0);
+                if (body + 2 * lane < Z.row_bytes) __stcs(reinterpret_cast<uint16_t*>(row + body) + lane, (uint16_t)0);
             }
+#pragma unroll 4
+            for (int64_t c = head + 16 * lane; c < body; c += 512)
+                __stcs(reinterpret_cast<uint4*>(row + c), make_uint4(0, 0, 0, 0));
         }
     }
 }
@@ -734,14 +745,17 @@ __global__ void __launch_bounds__(kSumThreads, 4) embed_sum_kernel(const __grid_
 #pragma unroll
             for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
         }
-    }    if constexpr (RING) cp_async_wait<0>();
+    }
+    if constexpr (RING) cp_async_wait<0>();
 }
 
 // The partial rows of long runs: that of the tile it begins in, then those of
 // the tiles it goes on through, in that order. A block takes 32 * CV columns
-// and the long runs that begin in kFixTiles tiles; its warps add contiguous
-// shares of a run's tiles, and the shares are added in order.
+// and the long runs that begin in kFixTiles tiles: each warp adds up runs of up
+// to kShortRun more tiles by itself; of the others, afterwards, every warp adds
+// a contiguous share, and the shares are added in order.
 constexpr int kFixTiles = 32;
+constexpr int kShortRun = 8;
 
 template <bool GB, int CV>
 __global__ void __launch_bounds__(kFixThreads) embed_fix_kernel(const __grid_constant__ SumArgs A) {
@@ -757,32 +771,56 @@ __global__ void __launch_bounds__(kFixThreads) embed_fix_kernel(const __grid_con
     const int64_t col = ((int64_t)(blockIdx.x % A.col_chunks) * 32 + lane) * CV;
     const bool in = col < A.dim;
     const int64_t g0 = (int64_t)(blockIdx.x / A.col_chunks) * kFixTiles;
-    uint32_t todo = __ballot_sync(0xffffffffu, g0 + lane < A.tiles && A.long_run[g0 + lane]);
-    for (; todo; todo &= todo - 1) {
-        const int64_t t0 = g0 + __ffs(todo) - 1;
-        const int32_t key = A.keys[(t0 + 1) * A.tile];
-        int64_t m = 0;  // tiles that the run goes on through
-        for (;; m += 32) {
-            const int64_t q = t0 + 1 + m + lane;
-            const uint32_t same = __ballot_sync(0xffffffffu, q < A.tiles && A.keys[q * A.tile] == key);
-            if (same != 0xffffffffu) {
-                m += __ffs(~same) - 1;
-                break;
-            }
+    auto key_of = [&](int64_t t0) { return A.keys[(t0 + 1) * A.tile]; };
+    // whether the run that goes on after tile t0 also covers the first token of tile t0 + 1 + more
+    auto reaches = [&](int64_t t0, int64_t more, int32_t key) {
+        const int64_t q = t0 + 1 + more;
+        return q < A.tiles && A.keys[q * A.tile] == key;
+    };
+    auto add = [&](int64_t t0, int64_t lo, int64_t hi, float (&acc)[CV]) {  // tiles t0 + 1 + lo .. t0 + hi
+#pragma unroll 8
+        for (int64_t q = lo; q < hi; ++q) {
+            float f[CV];
+            load_vec<false, CV>(A.slots, 2 * (t0 + 1 + q) * A.slot_ld + col, f);
+#pragma unroll
+            for (int e = 0; e < CV; ++e) acc[e] += f[e];
         }
+    };
+    uint32_t todo = __ballot_sync(0xffffffffu, g0 + lane < A.tiles && A.long_run[g0 + lane]);
+    // Every warp looks at every run (only those it adds up cost it more): bit k of `many`: the run that begins in
+    // tile k goes on through more than kShortRun tiles.
+    const bool mine = todo >> lane & 1u;
+    uint32_t many = __ballot_sync(0xffffffffu, mine && reaches(g0 + lane, kShortRun, key_of(g0 + lane)));
+    int turn = 0;
+    for (uint32_t few = todo & ~many; few; few &= few - 1, ++turn) {
+        if (turn % W != w) continue;
+        const int64_t t0 = g0 + __ffs(few) - 1;
+        const int32_t key = key_of(t0);
+        const int m = __popc(__ballot_sync(0xffffffffu, lane < kShortRun && reaches(t0, lane, key)));
+        if (!in) continue;
+        float acc[CV];
+        load_vec<false, CV>(A.slots, (2 * t0 + 1) * A.slot_ld + col, acc);
+        add(t0, 0, m, acc);
+        write_row<GB, CV>(A, key, col, acc);
+    }
+    for (; many; many &= many - 1) {
+        const int64_t t0 = g0 + __ffs(many) - 1;
+        const int32_t key = key_of(t0);
+        int64_t lo = kShortRun, hi = A.tiles - (t0 + 1);  // the run reaches lo more tiles, and not hi more
+        while (hi - lo > 1) {  // 32 probes a step
+            const int64_t width = (hi - lo + 32) / 33, probe = lo + width * (lane + 1);
+            const uint32_t yes = __ballot_sync(0xffffffffu, probe < hi && reaches(t0, probe, key));
+            const int n = __popc(yes);  // the first n probes are reached
+            hi = min(hi, lo + width * (n + 1));
+            lo += width * n;
+        }
+        const int64_t m = lo + 1;  // tiles that it goes on through
         float acc[CV];
 #pragma unroll
         for (int e = 0; e < CV; ++e) acc[e] = 0.f;
         if (in) {
             if (w == 0) load_vec<false, CV>(A.slots, (2 * t0 + 1) * A.slot_ld + col, acc);
-            const int64_t hi = m * (w + 1) / W;
-#pragma unroll 8
-            for (int64_t q = m * w / W; q < hi; ++q) {
-                float f[CV];
-                load_vec<false, CV>(A.slots, 2 * (t0 + 1 + q) * A.slot_ld + col, f);
-#pragma unroll
-                for (int e = 0; e < CV; ++e) acc[e] += f[e];
-            }
+            add(t0, m * w / W, m * (w + 1) / W, acc);
 #pragma unroll
             for (int e = 0; e < CV; ++e) part[w][lane * CV + e] = acc[e];
         }
@@ -806,20 +844,23 @@ struct LookupArgs {
     void* out;
     int64_t dim, ldt, ldo;
     float scale;
-    int32_t lanes_log2;  // threads per token row: 2^lanes_log2 of the block's 256
+    int32_t lanes;  // threads per token row, of the block's 256
 };
 
 constexpr int kLookupThreads = 256;
+
+constexpr int kLookupLoads = 4;  // in flight per thread
 
 template <bool TB, bool OB, int VEC, int TOKENS>
 __global__ void __launch_bounds__(kLookupThreads, 4) embed_lookup_kernel(const __grid_constant__ LookupArgs A) {
     griddep_launch_dependents();
     griddep_wait();
-    const int lanes = 1 << A.lanes_log2, t = threadIdx.x & (lanes - 1);
-    const int groups = kLookupThreads >> A.lanes_log2;
+    const int lanes = A.lanes, groups = kLookupThreads / lanes;
+    const int group = threadIdx.x / lanes, t = threadIdx.x - group * lanes;
+    if (group == groups) return;
     // this thread's rows: T of them, `groups` apart; their ids before anything depends on one
-    constexpr int T = TOKENS, U = 4 / TOKENS;
-    const int64_t i0 = (int64_t)blockIdx.x * groups * T + (threadIdx.x >> A.lanes_log2);
+    constexpr int T = TOKENS, U = kLookupLoads / TOKENS;
+    const int64_t i0 = (int64_t)blockIdx.x * groups * T + group;
     int64_t id[T];
     bool in[T], real[T];
 #pragma unroll
@@ -835,14 +876,15 @@ __global__ void __launch_bounds__(kLookupThreads, 4) embed_lookup_kernel(const _
         in[k] = real[k] && id[k] >= 0 && id[k] < A.ids.rows;
         if (real[k] && !in[k] && id[k] != A.ids.padding && t == 0) record_error(A.ids.status, MA_ERR_BOUNDS);
     }
-    for (int64_t c0 = (int64_t)t * VEC; c0 < A.dim; c0 += (int64_t)U * lanes * VEC) {
+    const int dim = (int)A.dim, step = lanes * VEC;
+    for (int c0 = t * VEC; c0 < dim; c0 += U * step) {
         float f[T][U][VEC];
 #pragma unroll
         for (int k = 0; k < T; ++k)
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int64_t c = c0 + (int64_t)u * lanes * VEC;
-                if (in[k] && c < A.dim &&
+                const int c = c0 + u * step;
+                if (in[k] && c < dim &&
                     MA_INB(id[k] * A.ldt + c, VEC, (A.ids.rows - 1) * A.ldt + A.dim, A.ids.status))
                     load_vec<TB, VEC>(A.table, id[k] * A.ldt + c, f[k][u]);
             }
@@ -850,8 +892,9 @@ __global__ void __launch_bounds__(kLookupThreads, 4) embed_lookup_kernel(const _
         for (int k = 0; k < T; ++k)
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int64_t c = c0 + (int64_t)u * lanes * VEC, i = i0 + k * groups;
-                if (!real[k] || c >= A.dim) continue;
+                const int c = c0 + u * step;
+                const int64_t i = i0 + k * groups;
+                if (!real[k] || c >= dim) continue;
 #pragma unroll
                 for (int e = 0; e < VEC; ++e) f[k][u][e] = in[k] ? f[k][u][e] * A.scale : 0.f;
                 if (MA_INB(i * A.ldo + c, VEC, (A.ids.n - 1) * A.ldo + A.dim, A.ids.status))
@@ -882,13 +925,17 @@ struct GradLayout {
     size_t off_k0, off_p0, off_k1, off_p1, off_hist, off_present, off_long, off_slots, total;
 };
 
-// Tokens per tile of the sum: the longest of 64, 32, 16 and 8 that still gives
-// six blocks of 256 threads to each of 148 SMs (a longer tile searches less
-// and leaves fewer partial rows; too few blocks leave SMs without loads in flight).
+// Tokens per tile of the sum, from 512 down to 8: the longest that still gives
+// six blocks of up to 256 threads to each of 148 SMs (a longer tile searches
+// less and leaves fewer partial rows; too few blocks leave SMs without loads in
+// flight), and twelve above 64 tokens, where a block lasts long and a last
+// round of few blocks would too. Against tiles of at most 64: 131,072 tokens x
+// 1280 bf16 of a skewed distribution 138 us (169), all the same token 161 (222);
+// 1,000,000 x 128 uniform 175 (157), all the same token 176 (901).
 int sum_tile(int64_t n, int64_t dim) {
     const int64_t col_blocks = (dim + 8 * kSumThreads - 1) / (8 * kSumThreads);
     int s = kMaxSumTile;
-    while (s > 8 && (n + s - 1) / s * col_blocks < 6 * 148) s /= 2;
+    while (s > 8 && (n + s - 1) / s * col_blocks < (s > 64 ? 12 : 6) * 148) s /= 2;
     return s;
 }
 
@@ -992,8 +1039,7 @@ ZeroPlan plan_zeros(void* grad, int64_t rows, int64_t dim, int64_t ldg, int gsz,
     z.ld_bytes = ldg * gsz;
     z.status = device_status_ptr();
     if (none) return P;
-    const uint64_t bits = reinterpret_cast<uintptr_t>(grad) | (uint64_t)z.row_bytes | (uint64_t)z.ld_bytes;
-    z.unit = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
+    z.aligned = (reinterpret_cast<uintptr_t>(grad) | (uint64_t)z.row_bytes | (uint64_t)z.ld_bytes) % 16 == 0;
     // two parts per SM, in whole words of the bit map, no more rows than the one-block sort's kernel has bits for
     z.period = ((rows + 2 * sms - 1) / (2 * sms) + 31) / 32 * 32;
     z.period = std::min<int64_t>(z.period, (int64_t)kSmallSortSmem * 8);
@@ -1077,11 +1123,14 @@ int lookup(int64_t n, const void* ids, int idt, int64_t rows, int64_t dim, const
     int vec = 1;
     for (int v : {8, 2})
         if (vec == 1 && rows_take(table, dim, ldt, tsz, v) && rows_take(out, dim, ldo, osz, v)) vec = v;
-    while (A.lanes_log2 < 8 && ((int64_t)vec << A.lanes_log2) < dim) ++A.lanes_log2;
-    // Two tokens a thread where a row takes at most two vectors of each of its threads and the batch fills the GPU
-    // either way: four loads in flight per thread instead of two.
-    const bool two = dim <= ((int64_t)2 * vec << A.lanes_log2) && (n << A.lanes_log2) >= (int64_t)2048 * 148;
-    const int64_t per_block = (int64_t)(two ? 2 : 1) << (8 - A.lanes_log2);
+    // Two tokens a thread where the batch fills the GPU either way: half of a thread's loads from each row, so that a
+    // row of 4096 bf16 takes a block's threads once.
+    // bf16, two against one: 131,072 tokens x 1280 124 us (306), 8192 x 4096 26.1 (32.5), 2048 x 4096 5.9 (7.2); 1024 x
+    // 4096, below the rule, 4.8 (4.8). What bounds it then is HBM: 8192 x 4096 distinct rows move 134 MB, 5.1 TB/s.
+    const int64_t vecs = dim / vec, each = kLookupLoads / 2;
+    const bool two = n * std::min<int64_t>(vecs, kLookupThreads) >= (int64_t)2048 * 148;
+    A.lanes = (int)std::min<int64_t>(kLookupThreads, two ? (vecs + each - 1) / each : vecs);
+    const int64_t per_block = (int64_t)(two ? 2 : 1) * (kLookupThreads / A.lanes);
     const dim3 grid((unsigned)((n + per_block - 1) / per_block)), block(kLookupThreads);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int pr = prof_begin(MA_PROF_EMBED, s);
