@@ -313,3 +313,48 @@ def test_arguments_that_do_not_fit():
         with pytest.raises(ma.MAError) as e:
             call()
         assert e.value.code == code
+
+
+@pytest.mark.parametrize("n,D", [(2000, 40), (60000, 8), (500000, 8), (1000000, 16), (1000003, 1)])
+def test_long_runs_of_every_length(n, D):
+    # runs through zero to many tiles of the sum (8 to 512 tokens each), several of them side by side, first and last
+    # in the batch's order, in rows whose ends are not at vectors' borders
+    r = np.random.default_rng(n)
+    lengths = []
+    while sum(lengths) < n:
+        lengths.append(int(min(n - sum(lengths), r.choice([1, 31, 33, 64, 257, 513, 600, 4097, 4700, n // 5]))))
+    V = len(lengths) + 3
+    rows = np.sort(r.permutation(V)[:len(lengths)])
+    ids = torch.from_numpy(r.permutation(np.repeat(rows, lengths))).cuda()
+    dy = torch.randn((n, D), generator=gen(n), device="cuda").bfloat16()
+    for ld in (D, D + 3):
+        full = torch.full((V, ld), 7.0, dtype=torch.bfloat16, device="cuda")
+        grad = full[:, :D]
+        ma.embedding_grad(ids, dy, grad)
+        check_grad(grad, *ref_grad(ids, dy, V, 1.0))
+        assert (full[:, D:] == 7).all()  # what lies between the rows stays
+    assert ma.ma_device_status() == ma.MA_OK
+
+
+@pytest.mark.parametrize("n", [5, 9000])
+@pytest.mark.parametrize("D", [1, 3, 7, 8, 9, 15, 1283])
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_zeros_of_rows_at_any_alignment(n, D, dt):
+    V, off, ld = 500, 3, D + 5
+    flat = torch.full((off + V * ld,), 7.0, dtype=DT[dt], device="cuda")
+    grad = flat[off:off + V * ld].view(V, ld)[:, :D]
+    ids = make_ids("uniform", n, V // 10)
+    dy = torch.randn((n, D), generator=gen(n), device="cuda").to(DT[dt])
+    ma.embedding_grad(ids, dy, grad)
+    check_grad(grad, *ref_grad(ids, dy, V, 1.0))
+    assert (flat[:off] == 7).all() and (flat[off:].view(V, ld)[:, D:] == 7).all()
+    assert ma.ma_device_status() == ma.MA_OK
+
+
+@pytest.mark.parametrize("n", [3, 700, 40000])
+@pytest.mark.parametrize("D", [1, 8, 24, 1280, 1282, 2056, 5000])
+def test_lookup_of_rows_that_do_not_fill_a_block(n, D):
+    table = torch.randn((300, D), generator=gen(D), device="cuda").bfloat16()
+    ids = make_ids("zipf", n, 300)
+    assert torch.equal(ma.embedding_lookup(ids, table), table[ids])  # a scale of one: the same bits
+    assert ma.ma_device_status() == ma.MA_OK
