@@ -35,6 +35,7 @@
 // (256-row blocks, half the keys loaded by each CTA) were slower, 58 us: each
 // product then waits for an arrival from the other CTA.
 #include <algorithm>
+#include <cfloat>
 #include <climits>
 #include <cmath>
 #include <cstring>
@@ -56,7 +57,8 @@ constexpr uint32_t kCtlBytes = 512;
 constexpr int kMaxChunks = 4;                  // head dimension up to 256
 constexpr int kMaxStages = 12;
 // Buffers for blocks of queries: where the shared memory allows, a third one, so
-// that the next segment's first block arrives while this one's are in use.
+// that the next segment's first block arrives while this one's are in use
+// (12 sequences of 500 tokens, 16 heads x 128: 10.5 us, 12.7 with two).
 constexpr int q_buffers(int ch) { return ch <= 2 ? 3 : 2; }
 // Stages of N keys x 64 columns that fit beside them.
 constexpr int stages(int n, int ch) {
@@ -70,21 +72,23 @@ constexpr long long kDrainNs = 50000000LL;  // bound of the waits for this CTA's
 // mbar_wait_ctl, for waits that are mostly over at once (wait) and, when not,
 // short. The timer is looked at only after 64 attempts that each slept up to
 // 1 us. False after the limit (recorded, and the abort raised) or, unless
-// `drain`, once another thread has raised the abort.
+// `drain`, once another warp has raised the abort. Whole warps wait, and every
+// lane gets the same answer: what follows a wait needs all of them.
 struct Waits {
     volatile int* abort;
     long long limit_ns;
     int* status;
 };
 __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, const Waits& W, long long limit_ns, bool drain) {
+    constexpr uint32_t kAll = 0xffffffffu;
     for (int it = 0; it < 64; ++it) {
-        if (mbar_try_wait_sleep(bar, parity, 1000u)) return true;
-        if (!drain && *W.abort) return false;
+        if (__all_sync(kAll, mbar_try_wait_sleep(bar, parity, 1000u))) return true;
+        if (!drain && __any_sync(kAll, *W.abort)) return false;
     }
     const uint64_t t0 = globaltimer();
-    while (!mbar_try_wait_sleep(bar, parity, 1000u)) {
-        if (!drain && *W.abort) return false;
-        if ((long long)(globaltimer() - t0) > limit_ns) {
+    while (!__all_sync(kAll, mbar_try_wait_sleep(bar, parity, 1000u))) {
+        if (!drain && __any_sync(kAll, *W.abort)) return false;
+        if (__any_sync(kAll, (long long)(globaltimer() - t0) > limit_ns)) {
             record_error(W.status, MA_ERR_TIMEOUT);
             *W.abort = 1;
             return false;
@@ -93,7 +97,7 @@ __device__ __noinline__ bool wait_on(uint32_t bar, uint32_t parity, const Waits&
     return true;
 }
 __device__ __forceinline__ bool wait(uint32_t bar, uint32_t parity, const Waits& W) {
-    return mbar_try_wait(bar, parity) || wait_on(bar, parity, W, W.limit_ns, false);
+    return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)) || wait_on(bar, parity, W, W.limit_ns, false);
 }
 
 struct QkLaunch {
@@ -656,8 +660,11 @@ struct QkScale {
     int* status;
 };
 
-// g = min(1, tau / S); a maximum that is not finite (or below -tau) leaves the weights alone
-__device__ __forceinline__ float gamma_of(float s, float tau) { return s > tau && s < INFINITY ? tau / s : 1.f; }
+// g = min(1, tau / S), at least the smallest normal number (a quotient that underflowed to 0 would make 0 / 0 of a
+// shared key head's factors); a maximum that is not finite leaves the weights alone
+__device__ __forceinline__ float gamma_of(float s, float tau) {
+    return s > tau && s < INFINITY ? fmaxf(tau / s, FLT_MIN) : 1.f;
+}
 __device__ __forceinline__ float share(float g, float e) { return g == 1.f ? 1.f : e == 0.5f ? sqrtf(g) : powf(g, e); }
 
 // Every block lists the heads whose factor is not 1, then takes its share of
@@ -820,13 +827,17 @@ int qk_max(int64_t seqs, int64_t len, int64_t total, int heads, int kv_heads, in
             if (st[i] >= (int64_t(1) << 38)) return MA_ERR_UNSUPPORTED;
         }
     }
+    const int n = tile_keys(dim);
+    const int chunks = (dim + kBK - 1) / kBK;
+    const int64_t m = (len + kRows - 1) / kRows;  // units of a (longest) sequence
+    const int64_t units =
+        (causal ? (n == 256 ? (m + 1) * (m + 1) / 4 : m * (m + 1) / 2) : m * ((len + n - 1) / n)) * heads;
+    if ((double)units * (double)seqs > 0x1p54) return MA_ERR_UNSUPPORTED;  // the kernel multiplies it by its grid
     int sms = 0;
     if (const int rc = device_ready(&sms)) return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     QkLaunch L;
     std::memset(&L, 0, sizeof(L));
-    const int n = tile_keys(dim);
-    const int chunks = (dim + kBK - 1) / kBK;
     if (work) {
         if (!make_map(&L.mq, q, dim, tokens, heads, outer, st[0], st[1], st[2], kRows) ||
             !make_map(&L.mk, k, dim, tokens, kv_heads, outer, st[3], st[4], st[5], n))
@@ -850,9 +861,6 @@ int qk_max(int64_t seqs, int64_t len, int64_t total, int heads, int kv_heads, in
         // a CTA per SM; fewer when there are fewer units (dense batches: the host knows)
         int grid = sms;
         if (!offsets) {
-            const int64_t m = (len + kRows - 1) / kRows;
-            const int64_t units = (causal ? (n == 256 ? (m + 1) * (m + 1) / 4 : m * (m + 1) / 2) : m * ((len + n - 1) / n)) *
-                                  heads;
             grid = (int)std::min<int64_t>(sms, units * std::min<int64_t>(seqs, sms));
             flops = 2.0 * dim * heads * (double)seqs * (causal ? 0.5 * len * (len + 1.0) : (double)len * len);
         }
@@ -887,6 +895,7 @@ int ma_qk_clip(int heads, int kv_heads, int64_t q_rows, int64_t k_rows, int64_t 
     if (!max_logit) return MA_ERR_NULL;
     QkScale A;
     std::memset(&A, 0, sizeof(A));
+    if (cols > 0 && std::max(q_rows, k_rows) > (int64_t(1) << 40) / cols) return MA_ERR_UNSUPPORTED;
     A.nq = q_rows * cols;
     A.nk = k_rows * cols;
     if ((A.nq > 0 && !wq) || (A.nk > 0 && !wk)) return MA_ERR_NULL;

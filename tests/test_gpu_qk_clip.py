@@ -257,6 +257,26 @@ def test_clip_scales_the_weights(H, KV, dq, dk, C, alpha, shift):
     assert ((fq * fk.repeat_interleave(H // KV) - gam).abs() <= 1e-12).all()
 
 
+@pytest.mark.parametrize("H,KV", [(2, 2), (4, 2)])
+def test_a_factor_below_the_smallest_number(H, KV):
+    # tau / S underflows: the factor is the smallest normal number, never 0 or 0 / 0
+    wq, wk = torch.full((H * 2, 8), 1e20, device="cuda"), torch.full((KV * 2, 8), 1e20, device="cuda")
+    top = torch.full((H,), 1e20, device="cuda")
+    top[1] = 0.5e-30
+    ma.qk_clip(wq, wk, top, tau=1e-30, alpha=0.5, kv_heads=KV)
+    tiny = torch.finfo(torch.float32).tiny  # 2^-126
+    fq, fk = (wq.view(H, -1)[:, 0].double() / 1e20).cpu(), (wk.view(KV, -1)[:, 0].double() / 1e20).cpu()
+    gam = torch.full((H,), tiny, dtype=torch.float64)
+    gam[1] = 1.0
+    want_k = gam.view(KV, -1).amin(dim=1) ** 0.5
+    want_q = gam / want_k.repeat_interleave(H // KV)
+    assert ((fk / want_k - 1).abs() <= 32 * U).all()
+    if H > KV:  # the head within tau: 1e20 * 2^63 = 9.2e38 is more than fp32 holds
+        assert torch.isinf(fq[1])
+        fq, want_q = torch.cat((fq[:1], fq[2:])), torch.cat((want_q[:1], want_q[2:]))
+    assert ((fq / want_q - 1).abs() <= 32 * U).all()
+
+
 def test_clipped_projection_gives_tau():
     # q = x W_q^T, k = x W_k^T: after the clip the largest logits are tau, up to the bf16 rounding of q and k
     T, H, KV, D, C = 500, 4, 2, 64, 96

@@ -31,7 +31,8 @@ def clip(heads=4, kv=2, q_rows=64, k_rows=64, cols=256, wq=WQ, wk=WK, top=OUT, t
     (dict(q=None), ma.MA_ERR_NULL), (dict(k=None), ma.MA_ERR_NULL), (dict(q=Q + 8), ma.MA_ERR_ALIGN),
     (dict(k=K + 2), ma.MA_ERR_ALIGN), (dict(q_tok=250), ma.MA_ERR_ALIGN), (dict(q_tok=32), ma.MA_ERR_SHAPE),
     (dict(k_head=0), ma.MA_ERR_SHAPE), (dict(k_seq=-8), ma.MA_ERR_SHAPE), (dict(q_seq=1 << 38), ma.MA_ERR_UNSUPPORTED),
-    (dict(offsets=OFF + 2, total=100), ma.MA_ERR_ALIGN)])
+    (dict(offsets=OFF + 2, total=100), ma.MA_ERR_ALIGN),
+    (dict(len=1 << 30, heads=1 << 11, kv=1 << 11), ma.MA_ERR_UNSUPPORTED)])
 def test_max_logit_refuses(kw, code):
     assert top(**kw) == code
 
@@ -39,7 +40,9 @@ def test_max_logit_refuses(kw, code):
 @pytest.mark.parametrize("kw,code", [
     (dict(heads=0), ma.MA_ERR_SHAPE), (dict(kv=3), ma.MA_ERR_SHAPE), (dict(q_rows=-1), ma.MA_ERR_SHAPE),
     (dict(cols=-1), ma.MA_ERR_SHAPE), (dict(heads=2048, kv=1), ma.MA_ERR_UNSUPPORTED),
-    (dict(cols=(1 << 30) + 1), ma.MA_ERR_UNSUPPORTED), (dict(tau=0.0), ma.MA_ERR_ARG), (dict(tau=math.nan), ma.MA_ERR_ARG),
+    (dict(cols=(1 << 30) + 1), ma.MA_ERR_UNSUPPORTED),
+    (dict(q_rows=1 << 30, cols=1 << 30), ma.MA_ERR_UNSUPPORTED), (dict(k_rows=1 << 30, cols=1 << 30), ma.MA_ERR_UNSUPPORTED),
+    (dict(tau=0.0), ma.MA_ERR_ARG), (dict(tau=math.nan), ma.MA_ERR_ARG),
     (dict(tau=math.inf), ma.MA_ERR_ARG), (dict(alpha=-0.1), ma.MA_ERR_ARG), (dict(alpha=1.1), ma.MA_ERR_ARG),
     (dict(alpha=math.nan), ma.MA_ERR_ARG), (dict(top=None), ma.MA_ERR_NULL), (dict(wq=None), ma.MA_ERR_NULL),
     (dict(wk=None), ma.MA_ERR_NULL), (dict(wq=WQ + 2), ma.MA_ERR_ALIGN), (dict(top=OUT + 1), ma.MA_ERR_ALIGN),
