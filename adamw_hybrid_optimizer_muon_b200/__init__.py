@@ -570,7 +570,7 @@ def _embedding_function():
 
     class Embedding(torch.autograd.Function):
         @staticmethod
-        def forward(ctx, ids, table, scale, padding, dtype, grad):
+        def forward(ctx, ids, table, scale, padding, dtype, grad, anchor):
             ctx.save_for_backward(ids)
             ctx.args = scale, padding, grad, table.shape, table.dtype, table.device
             return embedding_lookup(ids, table, scale, padding, dtype=dtype)
@@ -583,9 +583,9 @@ def _embedding_function():
             dy = dy.contiguous()
             if grad is not None:
                 embedding_grad(ids, dy, grad, scale, padding, accumulate=True)
-                return (None,) * 6
+                return (None,) * 7
             out = torch.empty(shape, dtype=dtype, device=device)
-            return None, embedding_grad(ids, dy, out, scale, padding), None, None, None, None
+            return None, embedding_grad(ids, dy, out, scale, padding), None, None, None, None, None
 
     _EMBEDDING = Embedding
     return Embedding
@@ -597,10 +597,21 @@ def embedding(ids, table, scale: float = 1.0, padding: int | None = None, dtype=
     ``grad``: a fp32 or bf16 buffer of the table's shape that backward adds the
     gradient to, in place of returning one: the buffer the optimizer reads can
     then be filled over several micro-batches, and no table-sized gradient is
-    made and added. The caller zeroes it, and it is complete when backward is."""
-    if grad is not None and (tuple(grad.shape) != tuple(table.shape)):
+    made and added. The caller zeroes it, and it is complete when backward is.
+
+    A backward pass captured into a CUDA graph: with ``grad``, at any time;
+    without, as with any operator of torch, only while no output of an earlier
+    uncaptured call on the table is still alive (torch refuses the capture)."""
+    if grad is None:
+        return _embedding_function().apply(ids, table, float(scale), padding, dtype, None, None)
+    if tuple(grad.shape) != tuple(table.shape):
         raise MAError(MA_ERR_SHAPE, "embedding: grad must have the table's shape")
-    return _embedding_function().apply(ids, table, float(scale), padding, dtype, grad)
+    # Autograd calls backward for a leaf of this call alone: torch binds a leaf to the stream of its first use, and
+    # the table's would tie a captured pass to the stream of an eager one.
+    torch = _torch()
+    needed = table.requires_grad and torch.is_grad_enabled()
+    anchor = torch.empty(0, device=table.device, requires_grad=True) if needed else None
+    return _embedding_function().apply(ids, table.detach(), float(scale), padding, dtype, grad, anchor)
 
 
 def qk_max_logit(q, k, scale: float | None = None, causal: bool = True, offsets=None, max_len: int | None = None,

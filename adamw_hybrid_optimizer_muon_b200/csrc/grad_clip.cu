@@ -260,21 +260,20 @@ __device__ __forceinline__ void take(const Chunk& k, const uint4* slots, uint4 (
 }
 
 // body(chunk, its slots) for the chunks of this block, kAhead - 1 of them in
-// flight meanwhile. backwards: from the last chunk of the table to the first.
+// flight meanwhile.
 template <int CAP, typename F>
-__device__ __forceinline__ void walk_chunks(const GradTable<CAP>& T, bool backwards, F body) {
+__device__ __forceinline__ void walk_chunks(const GradTable<CAP>& T, F body) {
     extern __shared__ uint4 ring[];
     const GradDesc* tab = table(T);
     const int nt = T.n;
     const int64_t n = T.nchunks, step = gridDim.x;
-    auto index = [&](int64_t q) { return backwards ? n - 1 - q : q; };
     int64_t ahead = blockIdx.x;
     int slot_ahead = 0, slot = 0;
     Cursor far, here;
     auto push = [&] {
         if (ahead < n) {
-            far.seek(tab, nt, n, index(ahead));
-            fetch(chunk_at(far.d, index(ahead)), ring + slot_ahead * (kThreads * kVecs), T.status);
+            far.seek(tab, nt, n, ahead);
+            fetch(chunk_at(far.d, ahead), ring + slot_ahead * (kThreads * kVecs), T.status);
         }
         cp_async_commit();  // a group per chunk, empty or not, so that the counts line up
         ahead += step;
@@ -285,8 +284,8 @@ __device__ __forceinline__ void walk_chunks(const GradTable<CAP>& T, bool backwa
     for (int64_t q = blockIdx.x; q < n; q += step) {
         push();
         cp_async_wait<kAhead - 1>();
-        here.seek(tab, nt, n, index(q));
-        body(chunk_at(here.d, index(q)), ring + slot * (kThreads * kVecs));
+        here.seek(tab, nt, n, q);
+        body(chunk_at(here.d, q), ring + slot * (kThreads * kVecs));
         slot = slot + 1 == kAhead ? 0 : slot + 1;
     }
     cp_async_wait<0>();
@@ -353,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) grad_sumsq_kernel(cons
     griddep_wait();
     __shared__ double red[kThreads / 32];
     double sum = 0.0;
-    walk_chunks(T, false, [&](const Chunk& k, const uint4* slots) {
+    walk_chunks(T, [&](const Chunk& k, const uint4* slots) {
         uint4 w[kVecs];
         if (k.bf16) {
             take<true>(k, slots, w, T.status);
@@ -442,11 +441,7 @@ cudaError_t clip_setup() {
     if (e != cudaSuccess) return e;
     return cache.get(dev, &done, [](int* v) {
         *v = 1;
-        const cudaError_t r = cudaFuncSetAttribute(grad_sumsq_kernel<CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   kRingBytes);
-        return r != cudaSuccess ? r
-                                : cudaFuncSetAttribute(grad_scale_kernel<CAP>,
-                                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+        return cudaFuncSetAttribute(grad_sumsq_kernel<CAP>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
     });
 }
 
@@ -640,8 +635,8 @@ cudaError_t launch_clip_finalize(const ClipArgs& a, int nparts, cudaStream_t s) 
     return e;
 }
 
-// The norm pass over items (numel > 0 each): partial sums, then either the
-// finalize (norm and coefficient) or the in-place scaling, which forms them itself.
+// The norm of items (numel > 0 each), and their scaling in place: one launch
+// for a small set; else partial sums, norm and coefficient, and the scaling.
 cudaError_t launch_grad_clip(const std::vector<GradItem>& items, const ClipArgs& args, int sms, bool in_place,
                              cudaStream_t s, int* launches) {
     ClipArgs a = args;

@@ -358,3 +358,39 @@ def test_lookup_of_rows_that_do_not_fill_a_block(n, D):
     ids = make_ids("zipf", n, 300)
     assert torch.equal(ma.embedding_lookup(ids, table), table[ids])  # a scale of one: the same bits
     assert ma.ma_device_status() == ma.MA_OK
+
+
+def test_captured_backward_while_an_eager_pass_lives():
+    table = torch.randn((90, 24), generator=gen(30), device="cuda", requires_grad=True)
+    ids = make_ids("zipf", 500, 90)
+    w = torch.randn((500, 24), generator=gen(31), device="cuda")
+    buf = torch.zeros((90, 24), device="cuda")
+    loss = lambda: (ma.embedding(ids, table, grad=buf) * w).sum()  # noqa: E731
+    loss().backward()  # the uncaptured passes: one done, one that still waits for its backward
+    want = buf.clone()
+    kept = loss()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        buf.zero_()
+        loss().backward()
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(buf, want)
+    kept.backward()
+    torch.cuda.synchronize()
+    s, a, c = ref_grad(ids, w, 90, 1.0)
+    check_grad(buf, s, a, c, want)
+    assert table.grad is None and ma.ma_device_status() == ma.MA_OK
+
+
+def test_nothing_needs_a_gradient():
+    table = torch.randn((9, 8), device="cuda")
+    ids = make_ids("uniform", 5, 9)
+    buf = torch.zeros((9, 8), device="cuda")
+    assert not ma.embedding(ids, table, grad=buf).requires_grad
+    table.requires_grad_()
+    with torch.no_grad():
+        assert not ma.embedding(ids, table, grad=buf).requires_grad
+    assert ma.embedding(ids, table, grad=buf).requires_grad and ma.embedding(ids, table).requires_grad
