@@ -626,15 +626,22 @@ __device__ __forceinline__ int lower_bound(const int32_t* k, int n, int32_t key)
     return lo;
 }
 
-template <bool YB, bool GB, int VEC>
+// Vectors of a row that a thread of the sums takes: four where they are narrow
+// and a row has more than a block of them, since the work per row and thread
+// then counts more than the loads. bf16, 131,072 tokens x 1281 columns: 233 us
+// (306 with one), x 1282: 182 (197); 50,000 x 300: 49 (38 with one, as it is).
+constexpr int sum_vectors(int vec, int64_t vecs) { return vec < 8 && vecs > kSumThreads ? 4 : 1; }
+
+template <bool YB, bool GB, int VEC, int K>
 __global__ void __launch_bounds__(kSumThreads, 4) embed_sum_kernel(const __grid_constant__ SumArgs A) {
     griddep_launch_dependents();
     griddep_wait();
     constexpr int kWin = kMaxSumTile + 2 * kLong;
     // Rows in flight: for vectors of 8, a ring of kRing 16-byte copies per thread in shared memory, four rows a
-    // step (cp.async; no thread reads another's slots, so there is no barrier); else eight rows in registers.
+    // step (cp.async; no thread reads another's slots, so there is no barrier); else four or eight rows in
+    // registers, of which a thread takes K narrow vectors each, blockDim apart.
     constexpr bool RING = VEC == 8;
-    constexpr int U = RING ? 4 : 8;
+    constexpr int U = RING || (K > 1 && Raw<YB, VEC>::kWords > 1) ? 4 : 8;
     constexpr int CPY = RING ? (YB ? 1 : 2) : 1;         // 16-byte copies per row
     constexpr int STEPS = RING ? kRing / (U * CPY) : 1;  // steps in the ring
     extern __shared__ uint4 ring[];
@@ -655,7 +662,8 @@ __global__ void __launch_bounds__(kSumThreads, 4) embed_sum_kernel(const __grid_
         if (q >= kLong && i < A.n) sp[q - kLong] = A.pos[i];
     }
     __syncthreads();
-    const int64_t col = ((int64_t)(block % A.col_blocks) * blockDim.x + threadIdx.x) * VEC;
+    const int64_t col = ((int64_t)(block % A.col_blocks) * blockDim.x * K + threadIdx.x) * VEC;
+    const int next = blockDim.x * VEC;  // columns between a thread's vectors
     // Tokens that add to no row are last; indexes below are relative to the tile.
     const int32_t rows = (int32_t)A.rows;
     const int32_t* tk = sk + kLong;
@@ -678,9 +686,11 @@ __global__ void __launch_bounds__(kSumThreads, 4) embed_sum_kernel(const __grid_
     }
     if (block % A.col_blocks == 0 && threadIdx.x == 0) A.long_run[tile] = tail_long;
     if (col >= A.dim) return;
-    float acc[VEC];
+    float acc[K][VEC];
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) acc[k][e] = 0.f;
     bool head = head_long;
     uint4* slots = ring + threadIdx.x;
     auto fetch = [&](int b, int step) {  // rows b .. b + U - 1 into a step of the ring
@@ -707,7 +717,7 @@ __global__ void __launch_bounds__(kSumThreads, 4) embed_sum_kernel(const __grid_
         ahead = STEPS - 1;
     }
     for (int b = begin; b < end; b += U) {
-        Raw<YB, VEC> f[U];
+        Raw<YB, VEC> f[U][K];
         if constexpr (RING) {
             fetch(b + (STEPS - 1) * U, ahead);
             ahead = ahead + 1 == STEPS ? 0 : ahead + 1;
@@ -715,14 +725,18 @@ __global__ void __launch_bounds__(kSumThreads, 4) embed_sum_kernel(const __grid_
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int c = 0; c < CPY; ++c) f[u].put(c, slots[((step * U + u) * CPY + c) * blockDim.x]);
+                for (int c = 0; c < CPY; ++c) f[u][0].put(c, slots[((step * U + u) * CPY + c) * blockDim.x]);
             step = step + 1 == STEPS ? 0 : step + 1;
         } else {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (b + u < end) {
                     const int64_t o = (int64_t)sp[b + u] * A.ldy + col;
-                    if (MA_INB(o, VEC, (A.n - 1) * A.ldy + A.dim, A.status)) f[u].load(A.dy, o);
+#pragma unroll
+                    for (int k = 0; k < K; ++k)
+                        if (col + k * next < A.dim &&
+                            MA_INB(o + k * next, VEC, (A.n - 1) * A.ldy + A.dim, A.status))
+                            f[u][k].load(A.dy, o + k * next);
                 }
             }
         }
@@ -730,20 +744,27 @@ __global__ void __launch_bounds__(kSumThreads, 4) embed_sum_kernel(const __grid_
         for (int u = 0; u < U; ++u) {
             const int i = b + u;
             if (i >= end) break;
-            f[u].add_to(acc);
+#pragma unroll
+            for (int k = 0; k < K; ++k) f[u][k].add_to(acc[k]);
             const int32_t key = tk[i];
             if (i + 1 < end && tk[i + 1] == key) continue;
             const bool tail = tail_long && i + 1 == end;
-            if (head || tail) {
-                float* slot = A.slots + (2 * (int64_t)tile + (head ? 0 : 1)) * A.slot_ld + col;
+            float* slot = A.slots + (2 * (int64_t)tile + (head ? 0 : 1)) * A.slot_ld + col;
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) slot[e] = acc[e];
-            } else {
-                write_row<GB, VEC>(A, key, col, acc);
+            for (int k = 0; k < K; ++k) {
+                if (k > 0 && col + k * next >= A.dim) break;
+                if (head || tail) {
+#pragma unroll
+                    for (int e = 0; e < VEC; ++e) slot[k * next + e] = acc[k][e];
+                } else {
+                    write_row<GB, VEC>(A, key, col + k * next, acc[k]);
+                }
             }
             head = false;
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+            for (int k = 0; k < K; ++k)
+#pragma unroll
+                for (int e = 0; e < VEC; ++e) acc[k][e] = 0.f;
         }
     }
     if constexpr (RING) cp_async_wait<0>();
@@ -987,7 +1008,7 @@ cudaError_t launch_sort_small(const SortArgs& A, unsigned grid, cudaStream_t s) 
     return launch_pdl(embed_sort_small_kernel, dim3(grid), dim3(kSortThreads), kSmallSortSmem, s, A);
 }
 
-template <bool YB, bool GB, int VEC>
+template <bool YB, bool GB, int VEC, int K>
 cudaError_t launch_sum(const SumArgs& A, unsigned grid, unsigned threads, cudaStream_t s) {
     const size_t ring = VEC == 8 ? (size_t)threads * kRing * 16 : 0;
     static PerDevice<int> cache;
@@ -996,11 +1017,11 @@ cudaError_t launch_sum(const SumArgs& A, unsigned grid, unsigned threads, cudaSt
     if (e != cudaSuccess) return e;
     e = cache.get(dev, &done, [](int* v) {
         *v = 1;
-        return cudaFuncSetAttribute(embed_sum_kernel<YB, GB, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(embed_sum_kernel<YB, GB, VEC, K>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     kSumThreads * kRing * 16);
     });
     if (e != cudaSuccess) return e;
-    return launch_pdl(embed_sum_kernel<YB, GB, VEC>, dim3(grid), dim3(threads), ring, s, A);
+    return launch_pdl(embed_sum_kernel<YB, GB, VEC, K>, dim3(grid), dim3(threads), ring, s, A);
 }
 
 // The parts of the zeros that the kernels write, in order: while the tokens are
@@ -1186,8 +1207,9 @@ int grad(int64_t n, const void* ids, int idt, int64_t rows, int64_t dim, const v
     S.status = device_status_ptr();
     S.tile = L.sum_tile;
     S.tiles = (int)L.sum_tiles;
-    // a thread takes one vector of a row: as few blocks of up to 256 threads across the columns as hold them all
-    const int64_t vecs = (dim + vec - 1) / vec;
+    // as few blocks of up to 256 threads across the columns as hold a row's vectors, `each` to a thread
+    const int each = sum_vectors(vec, dim / vec);
+    const int64_t vecs = (dim / vec + each - 1) / each;
     S.col_blocks = (int)((vecs + kSumThreads - 1) / kSumThreads);
     const unsigned threads = (unsigned)((vecs + S.col_blocks - 1) / S.col_blocks + 31) / 32 * 32;
     const int cv = std::min(vec, 4);
@@ -1261,7 +1283,11 @@ int grad(int64_t n, const void* ids, int idt, int64_t rows, int64_t dim, const v
         const unsigned grid = (unsigned)(S.zero.blocks + S.tiles * S.col_blocks);
         e = with_vec(vec, [&](auto v) {
             return with_types(ydt, gdt, [&](auto yb, auto gb) {
-                return launch_sum<decltype(yb)::value, decltype(gb)::value, decltype(v)::value>(S, grid, threads, s);
+                constexpr bool YB = decltype(yb)::value, GB = decltype(gb)::value;
+                constexpr int V = decltype(v)::value;
+                if constexpr (V < 8)
+                    if (each == 4) return launch_sum<YB, GB, V, 4>(S, grid, threads, s);
+                return launch_sum<YB, GB, V, 1>(S, grid, threads, s);
             });
         });
         S.zero = zeros.part(2);
