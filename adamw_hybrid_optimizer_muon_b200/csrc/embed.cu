@@ -36,9 +36,9 @@
 //
 // Measured, bf16: 8192 tokens x 4096 into 32,000 rows 75 us, of which the 262 MB
 // written take 61 at the 4.3 TB/s that plain stores reach on this GPU; 131,072 x
-// 1280 of a skewed distribution into 65,536 rows 138 us for 503 MB. Rows that are
+// 1280 of a skewed distribution into 65,536 rows 135 us for 503 MB. Rows that are
 // not whole 16-byte vectors go by two elements or by one, and issue bounds them:
-// uniform tokens of 1282 columns 189 us and of 1281 columns 309, of 1280 118.
+// uniform tokens of 1282 columns 190 us and of 1281 columns 237, of 1280 118.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -552,7 +552,7 @@ struct SumArgs {
     int64_t n, rows, dim, ldy, ldg, slot_ld;
     int64_t fix_blocks;  // last kernel: blocks that add partial rows; those after them write zeros
     ZeroShare zero;      // sums: the first blocks write zeros
-    int32_t tile, tiles, col_blocks, col_chunks, accumulate;
+    int32_t tile, tiles, col_blocks, col_chunks, fix_tiles, accumulate;
     float scale;
     int* status;
 };
@@ -772,14 +772,14 @@ __global__ void __launch_bounds__(kSumThreads, 4) embed_sum_kernel(const __grid_
 
 // The partial rows of long runs: that of the tile it begins in, then those of
 // the tiles it goes on through, in that order. A block takes 32 * CV columns
-// and the long runs that begin in kFixTiles tiles: each warp adds up runs of up
+// and the long runs that begin in up to kFixTiles tiles: each warp adds up runs of up
 // to kShortRun more tiles by itself; of the others, afterwards, every warp adds
 // a contiguous share, and the shares are added in order.
 constexpr int kFixTiles = 32;
 constexpr int kShortRun = 8;
 
 template <bool GB, int CV>
-__global__ void __launch_bounds__(kFixThreads) embed_fix_kernel(const __grid_constant__ SumArgs A) {
+__global__ void __launch_bounds__(kFixThreads, 5) embed_fix_kernel(const __grid_constant__ SumArgs A) {
     griddep_launch_dependents();
     griddep_wait();
     constexpr int W = kFixThreads / 32;
@@ -791,7 +791,7 @@ __global__ void __launch_bounds__(kFixThreads) embed_fix_kernel(const __grid_con
     __shared__ float part[W][32 * CV];
     const int64_t col = ((int64_t)(blockIdx.x % A.col_chunks) * 32 + lane) * CV;
     const bool in = col < A.dim;
-    const int64_t g0 = (int64_t)(blockIdx.x / A.col_chunks) * kFixTiles;
+    const int64_t g0 = (int64_t)(blockIdx.x / A.col_chunks) * A.fix_tiles;
     auto key_of = [&](int64_t t0) { return A.keys[(t0 + 1) * A.tile]; };
     // whether the run that goes on after tile t0 also covers the first token of tile t0 + 1 + more
     auto reaches = [&](int64_t t0, int64_t more, int32_t key) {
@@ -799,15 +799,21 @@ __global__ void __launch_bounds__(kFixThreads) embed_fix_kernel(const __grid_con
         return q < A.tiles && A.keys[q * A.tile] == key;
     };
     auto add = [&](int64_t t0, int64_t lo, int64_t hi, float (&acc)[CV]) {  // tiles t0 + 1 + lo .. t0 + hi
-#pragma unroll 8
-        for (int64_t q = lo; q < hi; ++q) {
-            float f[CV];
-            load_vec<false, CV>(A.slots, 2 * (t0 + 1 + q) * A.slot_ld + col, f);
+        constexpr int R = 16 / CV;  // rows in flight
+        for (int64_t q = lo; q < hi; q += R) {
+            float f[R][CV];
 #pragma unroll
-            for (int e = 0; e < CV; ++e) acc[e] += f[e];
+            for (int r = 0; r < R; ++r)
+                if (q + r < hi) load_vec<false, CV>(A.slots, 2 * (t0 + 1 + q + r) * A.slot_ld + col, f[r]);
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                if (q + r >= hi) break;
+#pragma unroll
+                for (int e = 0; e < CV; ++e) acc[e] += f[r][e];
+            }
         }
     };
-    uint32_t todo = __ballot_sync(0xffffffffu, g0 + lane < A.tiles && A.long_run[g0 + lane]);
+    uint32_t todo = __ballot_sync(0xffffffffu, lane < A.fix_tiles && g0 + lane < A.tiles && A.long_run[g0 + lane]);
     // Every warp looks at every run (only those it adds up cost it more): bit k of `many`: the run that begins in
     // tile k goes on through more than kShortRun tiles.
     const bool mine = todo >> lane & 1u;
@@ -947,16 +953,19 @@ struct GradLayout {
 };
 
 // Tokens per tile of the sum, from 512 down to 8: the longest that still gives
-// six blocks of up to 256 threads to each of 148 SMs (a longer tile searches
-// less and leaves fewer partial rows; too few blocks leave SMs without loads in
-// flight), and twelve above 64 tokens, where a block lasts long and a last
-// round of few blocks would too. Against tiles of at most 64: 131,072 tokens x
-// 1280 bf16 of a skewed distribution 138 us (169), all the same token 161 (222);
-// 1,000,000 x 128 uniform 175 (157), all the same token 176 (901).
+// each of 148 SMs six blocks and sixteen warps (a longer tile searches less and
+// leaves fewer partial rows; too few leave SMs without loads in flight), and
+// twice that above 64 tokens, where a block lasts long and a last round of few
+// blocks would too. Against tiles of at most 64: 131,072 tokens x 1280 bf16 of a
+// skewed distribution 135 us (169), all the same token 161 (222); 1,000,000 x
+// 128 skewed 162 (193), all the same token 301 (901). Sixteen warps, against six
+// blocks alone: 20,000 x 64 skewed 35.5 (38.7), 1,000,000 x 128 162 (185), all
+// the same token 301 (176).
 int sum_tile(int64_t n, int64_t dim) {
-    const int64_t col_blocks = (dim + 8 * kSumThreads - 1) / (8 * kSumThreads);
+    const int64_t warps = (dim + 255) / 256, blocks = (warps + 7) / 8;  // of a row, 8 elements to a thread
     int s = kMaxSumTile;
-    while (s > 8 && (n + s - 1) / s * col_blocks < (s > 64 ? 12 : 6) * 148) s /= 2;
+    auto fills = [&](int64_t tiles, int sms) { return tiles * blocks >= 6 * sms && tiles * warps >= 16 * sms; };
+    while (s > 8 && !fills((n + s - 1) / s, s > 64 ? 2 * 148 : 148)) s /= 2;
     return s;
 }
 
@@ -1209,13 +1218,17 @@ int grad(int64_t n, const void* ids, int idt, int64_t rows, int64_t dim, const v
     S.tiles = (int)L.sum_tiles;
     // as few blocks of up to 256 threads across the columns as hold a row's vectors, `each` to a thread
     const int each = sum_vectors(vec, dim / vec);
-    const int64_t vecs = (dim / vec + each - 1) / each;
-    S.col_blocks = (int)((vecs + kSumThreads - 1) / kSumThreads);
-    const unsigned threads = (unsigned)((vecs + S.col_blocks - 1) / S.col_blocks + 31) / 32 * 32;
+    const int64_t lanes = (dim / vec + each - 1) / each;
+    S.col_blocks = (int)((lanes + kSumThreads - 1) / kSumThreads);
+    const unsigned threads = (unsigned)((lanes + S.col_blocks - 1) / S.col_blocks + 31) / 32 * 32;
     const int cv = std::min(vec, 4);
     S.col_chunks = (int)((dim + 32 * cv - 1) / (32 * cv));
-    const int64_t sum_blocks = (int64_t)S.tiles * S.col_blocks;
-    S.fix_blocks = S.tiles > 1 ? (int64_t)((S.tiles + kFixTiles - 1) / kFixTiles) * S.col_chunks : 0;
+    // tiles whose long runs a block of the last kernel adds up: fewer where there would be less than a block per SM
+    // (100,000 tokens x 5: 43 us, 50 with 32 tiles a block)
+    S.fix_tiles = kFixTiles;
+    while (S.fix_tiles > kFixThreads / 32 && (S.tiles + S.fix_tiles - 1) / S.fix_tiles * (int64_t)S.col_chunks < sms)
+        S.fix_tiles /= 2;
+    S.fix_blocks = S.tiles > 1 ? (int64_t)((S.tiles + S.fix_tiles - 1) / S.fix_tiles) * S.col_chunks : 0;
     uint32_t* present = n > 0 ? at32(L.off_present) : nullptr;
     const ZeroPlan zeros = plan_zeros(g, rows, dim, ldg, gsz, present, accumulate != 0, sms);
     if ((int64_t)S.tiles * S.col_blocks + zeros.z.blocks > INT32_MAX || S.fix_blocks + zeros.z.blocks > INT32_MAX)
