@@ -38,7 +38,7 @@
 // written take 61 at the 4.3 TB/s that plain stores reach on this GPU; 131,072 x
 // 1280 of a skewed distribution into 65,536 rows 135 us for 503 MB. Rows that are
 // not whole 16-byte vectors go by two elements or by one, and issue bounds them:
-// uniform tokens of 1282 columns 190 us and of 1281 columns 237, of 1280 118.
+// uniform tokens of 1282 columns 196 us and of 1281 columns 237, of 1280 118.
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -626,11 +626,15 @@ __device__ __forceinline__ int lower_bound(const int32_t* k, int n, int32_t key)
     return lo;
 }
 
-// Vectors of a row that a thread of the sums takes: four where they are narrow
-// and a row has more than a block of them, since the work per row and thread
-// then counts more than the loads. bf16, 131,072 tokens x 1281 columns: 233 us
-// (306 with one), x 1282: 182 (197); 50,000 x 300: 49 (38 with one, as it is).
-constexpr int sum_vectors(int vec, int64_t vecs) { return vec < 8 && vecs > kSumThreads ? 4 : 1; }
+// Vectors of a row that a thread of the sums takes: four where they are narrow,
+// a row has over a thousand of them and the batch fills the GPU; the work per
+// row and thread then counts more than the loads in flight. Measured with four
+// (one): 1281 columns, 60,000 tokens 148 us (161), 8192 57 (66), 3000 36 (33),
+// 301 22 (13: the larger code takes longer to arrive); 4095 columns, 8192 tokens
+// 87 (118); 1282 columns, 641 vectors, 60,000 tokens 129 (109).
+constexpr int sum_vectors(int vec, int64_t vecs, int64_t n) {
+    return vec < 8 && vecs > 1024 && n * vecs > (1 << 22) ? 4 : 1;
+}
 
 template <bool YB, bool GB, int VEC, int K>
 __global__ void __launch_bounds__(kSumThreads, 4) embed_sum_kernel(const __grid_constant__ SumArgs A) {
@@ -1217,7 +1221,7 @@ int grad(int64_t n, const void* ids, int idt, int64_t rows, int64_t dim, const v
     S.tile = L.sum_tile;
     S.tiles = (int)L.sum_tiles;
     // as few blocks of up to 256 threads across the columns as hold a row's vectors, `each` to a thread
-    const int each = sum_vectors(vec, dim / vec);
+    const int each = sum_vectors(vec, dim / vec, n);
     const int64_t lanes = (dim / vec + each - 1) / each;
     S.col_blocks = (int)((lanes + kSumThreads - 1) / kSumThreads);
     const unsigned threads = (unsigned)((lanes + S.col_blocks - 1) / S.col_blocks + 31) / 32 * 32;

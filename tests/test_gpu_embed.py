@@ -394,3 +394,17 @@ def test_nothing_needs_a_gradient():
     with torch.no_grad():
         assert not ma.embedding(ids, table, grad=buf).requires_grad
     assert ma.embedding(ids, table, grad=buf).requires_grad and ma.embedding(ids, table).requires_grad
+
+
+@pytest.mark.parametrize("kind", ["zipf", "two", "uniform"])
+@pytest.mark.parametrize("n,D", [(5000, 2058), (4200, 1027), (4200, 4099)])
+@pytest.mark.parametrize("ydt,gdt", [("bf16", "fp32"), ("fp32", "bf16")])
+def test_wide_rows_of_narrow_vectors(n, D, kind, ydt, gdt):
+    # rows of more than 1024 vectors of one or two elements: a thread takes four of them
+    V = 700
+    ids = make_ids(kind, n, V)
+    dy = (torch.randn((n, D), generator=gen(n), device="cuda") * 1e-2).to(DT[ydt])
+    grad = torch.full((V, D), math.nan, dtype=DT[gdt], device="cuda")
+    ma.embedding_grad(ids, dy, grad, scale=0.5)
+    check_grad(grad, *ref_grad(ids, dy, V, 0.5))
+    assert ma.ma_device_status() == ma.MA_OK
