@@ -10,6 +10,8 @@ from __future__ import annotations
 
 import array
 import contextlib
+import importlib.machinery
+import importlib.util
 import ctypes
 import math
 import os
@@ -203,12 +205,50 @@ def _ptr(x) -> int:
 
 def _ptr_array(xs) -> ctypes.Array:
     try:
-        ptrs = array.array("Q", map(_torch().Tensor.data_ptr, xs))
+        ptrs = _marshal().pointers(xs)
     except TypeError:  # plain addresses, or None, among them
-        ptrs = array.array("Q", map(_ptr, xs))
-    if not ptrs:
-        ptrs.append(0)
-    return (ctypes.c_void_p * len(ptrs)).from_buffer(ptrs)
+        ptrs = bytearray(array.array("Q", map(_ptr, xs)))
+    return (ctypes.c_void_p * max(1, len(ptrs) // 8)).from_buffer(ptrs or bytearray(8))
+
+
+def _numel_array(xs) -> ctypes.Array:
+    """Element counts of tensors."""
+    try:
+        counts = _marshal().numels(xs)
+    except TypeError:
+        counts = bytearray(array.array("q", [int(x.numel()) for x in xs]))
+    return (ctypes.c_int64 * max(1, len(counts) // 8)).from_buffer(counts or bytearray(8))
+
+
+class _Methods:
+    """What the extension module does, through the tensors' methods."""
+
+    @staticmethod
+    def pointers(xs):
+        return bytearray(array.array("Q", map(_torch().Tensor.data_ptr, xs)))
+
+    @staticmethod
+    def numels(xs):
+        return bytearray(array.array("q", map(_torch().Tensor.numel, xs)))
+
+
+_MARSHAL = None
+
+
+def _marshal():
+    """The extension module that reads lists of tensors (lib/_marshal.so), or the methods in its place."""
+    global _MARSHAL
+    if _MARSHAL is None:
+        _torch()  # whose libraries it is linked to
+        path = os.path.join(os.path.dirname(LIB_PATH), "_marshal.so")
+        try:
+            loader = importlib.machinery.ExtensionFileLoader("_marshal", path)
+            module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_marshal", path, loader=loader))
+            loader.exec_module(module)
+            _MARSHAL = module
+        except ImportError:  # not built, or against another torch
+            _MARSHAL = _Methods
+    return _MARSHAL
 
 
 _TORCH = None
@@ -380,9 +420,7 @@ def adamw_step_fused(P, G, M, V, hp: AdamWHParams, stream=None, gdt: int | None 
     n = len(P)
     if gdt is None:
         gdt = _dtype_code(G[0]) if n else MA_F32
-    if numel is None:
-        numel = map(_torch().Tensor.numel, P)
-    nar = (ctypes.c_int64 * max(1, n)).from_buffer(array.array("q", numel) or array.array("q", [0]))
+    nar = _numel_array(P) if numel is None else (ctypes.c_int64 * max(1, n))(*numel)
     _check(lib().adamw_step_fused_clipped(n, _ptr_array(P), _ptr_array(G), int(gdt), _ptr_array(M), _ptr_array(V),
                                           nar, ctypes.byref(hp), _ptr(clip), _stream(stream)), "adamw_step_fused")
 
@@ -415,8 +453,7 @@ def _grad_tables(G):
     for g in G:
         if not g.is_contiguous():
             raise MAError(MA_ERR_SHAPE, "gradients must be contiguous")
-    return (n, _ptr_array(G), (ctypes.c_int32 * max(1, n))(*[_dtype_code(g) for g in G]),
-            (ctypes.c_int64 * max(1, n))(*[int(g.numel()) for g in G]))
+    return n, _ptr_array(G), (ctypes.c_int32 * max(1, n))(*[_dtype_code(g) for g in G]), _numel_array(G)
 
 
 def ma_grad_norm(G, clip, max_norm: float = math.inf, scale: float = 1.0, stream=None) -> None:

@@ -8,7 +8,8 @@ into ``lib/libmuonadamw.so``, and once more with ``-DMA_DEBUG`` into
 index against the extent of its buffer (a failed check records MA_ERR_BOUNDS
 and skips the access) and otherwise computes the same bits. Each object is
 rebuilt only when a source or header is newer than it; the objects compile in
-parallel. nvcc cross-compiles, so no GPU is needed.
+parallel. nvcc cross-compiles, so no GPU is needed. ``csrc/marshal.cpp`` becomes
+``lib/_marshal.so``, a Python extension module built against the installed torch.
 """
 from __future__ import annotations
 
@@ -18,6 +19,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -25,6 +27,7 @@ CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB_DIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIB_DIR, "libmuonadamw.so")
+MARSHAL = os.path.join(LIB_DIR, "_marshal.so")
 LIB_DEBUG = os.path.join(LIB_DIR, "libmuonadamw_debug.so")
 VARIANTS = (("release", LIB, []), ("debug", LIB_DEBUG, ["-DMA_DEBUG"]))
 
@@ -45,9 +48,28 @@ def _headers():
         glob.glob(os.path.join(ROOT, "include", "*.h"))
 
 
+def _build_marshal(verbose: bool, force: bool) -> None:
+    """The extension module that reads lists of tensors (the binding does without it, more slowly)."""
+    src = os.path.join(CSRC, "marshal.cpp")
+    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= os.path.getmtime(src):
+        return
+    import torch
+    base = os.path.join(os.path.dirname(torch.__file__))
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-w",
+           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(base, "include"),
+           "-I" + os.path.join(base, "include", "torch", "csrc", "api", "include"), src, "-o", MARSHAL,
+           "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if verbose or res.returncode != 0:
+        sys.stderr.write(res.stdout + res.stderr)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed on marshal.cpp")
+
+
 def build(verbose: bool = False, force: bool = False) -> str:
-    """Build both libraries; returns the release library's path."""
+    """Build both libraries and the extension module; returns the release library's path."""
     os.makedirs(LIB_DIR, exist_ok=True)
+    _build_marshal(verbose, force)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     hdr_mtime = max([os.path.getmtime(h) for h in _headers()] + [0.0])
     jobs = []  # (source, object, extra flags)
