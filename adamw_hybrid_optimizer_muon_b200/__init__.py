@@ -631,8 +631,8 @@ def _embedding_function():
 def embedding(ids, table, scale: float = 1.0, padding: int | None = None, dtype=None, grad=None):
     """embedding_lookup with a gradient for the table (embedding_grad; not differentiable twice).
 
-    ``grad``: a fp32 or bf16 buffer of the table's shape that backward adds the
-    gradient to, in place of returning one: the buffer the optimizer reads can
+    ``grad``: a fp32 or bf16 buffer of the shape of the table (which requires
+    grad) that backward adds the gradient to, in place of returning one: the buffer the optimizer reads can
     then be filled over several micro-batches, and no table-sized gradient is
     made and added. The caller zeroes it, and it is complete when backward is.
 

@@ -408,3 +408,21 @@ def test_wide_rows_of_narrow_vectors(n, D, kind, ydt, gdt):
     ma.embedding_grad(ids, dy, grad, scale=0.5)
     check_grad(grad, *ref_grad(ids, dy, V, 0.5))
     assert ma.ma_device_status() == ma.MA_OK
+
+
+@pytest.mark.parametrize("n", [1, 2, 31, 32, 33, 65, 320])
+@pytest.mark.parametrize("kind", ["one", "two", "zipf", "blocks"])
+@pytest.mark.parametrize("D", [5, 72, 2058, 100003])
+def test_short_batches(n, kind, D):
+    # up to 32 tokens no run is cut, and no kernel adds up partial rows
+    V = 40
+    ids = make_ids(kind, n, V) if kind != "blocks" else torch.arange(n, device="cuda") // 40
+    dy = torch.randn((n, D), generator=gen(n + D), device="cuda").bfloat16()
+    grad = torch.full((V, D), math.nan, device="cuda")
+    ma.embedding_grad(ids, dy, grad)
+    s, a, c = ref_grad(ids, dy, V, 1.0)
+    check_grad(grad, s, a, c)
+    old = grad.clone()
+    ma.embedding_grad(ids, dy, grad, accumulate=True)
+    check_grad(grad, s, a, c, old)
+    assert ma.ma_device_status() == ma.MA_OK
