@@ -17,9 +17,8 @@
 // shared memory, key and position packed into 32 bits; more by tiles of 1024, a
 // histogram, a scan and a scatter launch per digit. Digits have up to nine bits:
 // a vocabulary below 2^18 takes two passes. A whole gradient of 32,000 x 128
-// bf16 by the one block (by the tiles): 100 tokens 12.4 us (26.9), 2048 15.0
-// (31.2), 8192 25.9 (33.2); the one block's time grows with the tokens, and 8192
-// keys and their digit counts are what its shared memory is laid out for.
+// bf16 by the one block (by the tiles): 100 tokens 12.5 us (20.5), 2048 15.3
+// (24.2), 8192 26.1 (26.5).
 //
 // Sum. The sorted tokens are cut into tiles of S. A block takes one tile and a
 // range of columns and adds up the runs of equal tokens that begin in its tile,
@@ -36,7 +35,7 @@
 //
 // Measured, bf16: 8192 tokens x 4096 into 32,000 rows 75 us, of which the 262 MB
 // written take 61 at the 4.3 TB/s that plain stores reach on this GPU; 131,072 x
-// 1280 of a skewed distribution into 65,536 rows 135 us for 503 MB. Rows that are
+// 1280 of a skewed distribution into 65,536 rows 129 us for 503 MB. Rows that are
 // not whole 16-byte vectors go by two elements or by one, and issue bounds them:
 // uniform tokens of 1282 columns 196 us and of 1281 columns 237, of 1280 118.
 #include <algorithm>
@@ -59,8 +58,11 @@ constexpr int kPosBits = 13;
 constexpr int kSmallKeyBits = 32 - kPosBits;
 constexpr int kMaxDigitBits = 9;
 constexpr int kMaxDigits = 1 << kMaxDigitBits;
-constexpr int kTileThreads = 128;
-constexpr int kTile = kTileThreads * 8;  // tokens a block ranks at a time
+// Two tokens a thread: ranking goes token by token within a warp, so more warps
+// shorten it (131,072 skewed tokens of 65,536 rows x 1280, the whole gradient:
+// 132 us, four tokens 136, eight 142).
+constexpr int kTileThreads = 512;
+constexpr int kTile = kTileThreads * 2;  // tokens a block ranks at a time
 constexpr int kMaxTiles = 4096;          // tiles of a pass; longer batches have longer tiles
 constexpr int kSumThreads = 256;         // at most
 constexpr int kFixThreads = 256;
@@ -436,7 +438,8 @@ __global__ void __launch_bounds__(kTileThreads) embed_scan_kernel(const __grid_c
     if (lane == 0) A.totals[d] = run;
 }
 
-constexpr int kMarkWords = 8192;  // rows of a table up to 32 times this are marked by way of shared memory
+// rows of a table up to 32 times this are marked by way of shared memory (what is left of 48 KB)
+constexpr int kMarkWords = 7168;
 
 __global__ void __launch_bounds__(kTileThreads) embed_scatter_kernel(const __grid_constant__ TileArgs A) {
     griddep_launch_dependents();
@@ -447,6 +450,7 @@ __global__ void __launch_bounds__(kTileThreads) embed_scatter_kernel(const __gri
     __shared__ __align__(16) uint16_t hist[W * kMaxDigits];
     __shared__ uint32_t base[kMaxDigits];
     __shared__ uint32_t warp_sums[32];
+    static_assert(sizeof(hist) + sizeof(base) + sizeof(warp_sums) + 4 * kMarkWords <= 48 * 1024);
     if ((int)blockIdx.x >= A.tiles) {
         write_zeros(A.zero, blockIdx.x - A.tiles);
         return;
