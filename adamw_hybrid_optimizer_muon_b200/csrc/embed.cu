@@ -33,7 +33,7 @@
 // rows have tokens on (a bit per row) writes a share beside its own work, the
 // sums the rest.
 //
-// Measured, bf16: 8192 tokens x 4096 into 32,000 rows 75 us, of which the 262 MB
+// Measured, bf16: 8192 tokens x 4096 into 32,000 rows 72 us, of which the 262 MB
 // written take 61 at the 4.3 TB/s that plain stores reach on this GPU; 131,072 x
 // 1280 of a skewed distribution into 65,536 rows 129 us for 503 MB. Rows that are
 // not whole 16-byte vectors go by two elements or by one, and issue bounds them:
@@ -1042,9 +1042,12 @@ cudaError_t launch_sum(const SumArgs& A, unsigned grid, unsigned threads, cudaSt
 }
 
 // The parts of the zeros that the kernels write, in order: while the tokens are
-// sorted, beside the sums, and beside the last kernel. Sort and last kernel
-// last about as long as HBM takes for kSortHides and kLastHides bytes (small
-// batches: the whole sort; by tiles: what comes after the first scatter).
+// sorted, beside the sums, and beside the last kernel. Beside the sort by tiles
+// (what comes after its first scatter) and the last kernel go as many bytes as
+// HBM takes in their time; beside the one-block sort more, since its launch has
+// the GPU but for one SM, and the sums have loads to wait for: 8192 tokens x 4096
+// into 32,000 rows 72.5 us (77.5 with 60 MB there), 1000 tokens 60.5 (65.3).
+// 32,768 tokens by tiles: 122.5 (125.7 with 105 MB).
 struct ZeroPlan {
     ZeroShare z;
     int64_t cut[4];  // rows of each part: [cut[0], cut[1]) by the first kernels, ...
@@ -1064,9 +1067,10 @@ struct ZeroPlan {
         return s;
     }
 };
-constexpr double kSortHides = 60e6, kLastHides = 30e6;
+constexpr double kSmallSortHides = 110e6, kTileSortHides = 60e6, kLastHides = 30e6;
 
-ZeroPlan plan_zeros(void* grad, int64_t rows, int64_t dim, int64_t ldg, int gsz, uint32_t* present, bool none, int sms) {
+ZeroPlan plan_zeros(void* grad, int64_t rows, int64_t dim, int64_t ldg, int gsz, uint32_t* present, bool none,
+                    double sort_hides, int sms) {
     ZeroPlan P;
     std::memset(&P, 0, sizeof(P));
     ZeroShare& z = P.z;
@@ -1083,7 +1087,7 @@ ZeroPlan plan_zeros(void* grad, int64_t rows, int64_t dim, int64_t ldg, int gsz,
     z.period = std::min<int64_t>(z.period, (int64_t)kSmallSortSmem * 8);
     z.blocks = (int32_t)((rows + z.period - 1) / z.period);
     const double bytes = (double)rows * z.row_bytes;
-    const int64_t first = (int64_t)std::min((double)z.period, std::ceil(z.period * kSortHides / bytes));
+    const int64_t first = (int64_t)std::min((double)z.period, std::ceil(z.period * sort_hides / bytes));
     const int64_t last = (int64_t)std::min((double)(z.period - first), std::ceil(z.period * kLastHides / bytes));
     P.cut[0] = 0;
     P.cut[1] = first;
@@ -1240,7 +1244,8 @@ int grad(int64_t n, const void* ids, int idt, int64_t rows, int64_t dim, const v
     const bool whole = n <= kLong;
     S.fix_blocks = S.tiles > 1 && !whole ? (int64_t)((S.tiles + S.fix_tiles - 1) / S.fix_tiles) * S.col_chunks : 0;
     uint32_t* present = n > 0 ? at32(L.off_present) : nullptr;
-    const ZeroPlan zeros = plan_zeros(g, rows, dim, ldg, gsz, present, accumulate != 0, sms);
+    const ZeroPlan zeros = plan_zeros(g, rows, dim, ldg, gsz, present, accumulate != 0,
+                                      L.small ? kSmallSortHides : kTileSortHides, sms);
     if ((int64_t)S.tiles * S.col_blocks + zeros.z.blocks > INT32_MAX || S.fix_blocks + zeros.z.blocks > INT32_MAX)
         return MA_ERR_UNSUPPORTED;
     if (n > 0) {
