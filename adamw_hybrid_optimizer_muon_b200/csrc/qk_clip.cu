@@ -791,7 +791,8 @@ cudaError_t launch_max_ch(const QkLaunch& L, bool causal, bool abs, int grid, cu
 }
 
 // Keys per tile: 256, or 128 for head dimensions above 192, whose key tile of
-// 256 would not fit beside the queries.
+// 256 would not fit beside the queries. (4096 causal tokens, 32 heads of 64: 35
+// us, 45 with tiles of 128: the time between two products is per product.)
 int tile_keys(int dim) { return dim > 192 ? 128 : 256; }
 
 }  // namespace
