@@ -889,7 +889,7 @@ int ma_qk_max_logit(int64_t seqs, int64_t len, int64_t total, int heads, int kv_
 int ma_qk_clip(int heads, int kv_heads, int64_t q_rows, int64_t k_rows, int64_t cols, float* wq, float* wk,
                const float* max_logit, float tau, float alpha, void* stream) {
     if (heads < 1 || kv_heads < 1 || heads % kv_heads != 0 || q_rows < 0 || k_rows < 0 || cols < 0) return MA_ERR_SHAPE;
-    if (heads + kv_heads > kMaxHeads || q_rows > (int64_t(1) << 30) || k_rows > (int64_t(1) << 30) ||
+    if ((int64_t)heads + kv_heads > kMaxHeads || q_rows > (int64_t(1) << 30) || k_rows > (int64_t(1) << 30) ||
         cols > (int64_t(1) << 30))
         return MA_ERR_UNSUPPORTED;
     if (!(tau > 0.f) || !std::isfinite(tau) || !(alpha >= 0.f && alpha <= 1.f)) return MA_ERR_ARG;
