@@ -371,8 +371,9 @@ def muon_step_batched(W, G, M, hp: MuonHParams, ws, ws_bytes: int | None = None,
         gdt = _dtype_code(G[0]) if batch else MA_F32
     if ws_bytes is None:
         ws_bytes = ws.numel() * ws.element_size() if ws is not None else 0
+    coef = _clip_ptr("muon_step_batched", clip, CLIP_HEAD_BYTES, _on_current_gpu)
     _check(lib().muon_step_batched_clipped(batch, R, C, _ptr_array(W), _ptr_array(G), int(gdt), _ptr_array(M),
-                                           ctypes.byref(hp), _ptr(clip), _ptr(ws), int(ws_bytes), _stream(stream)),
+                                           ctypes.byref(hp), coef, _ptr(ws), int(ws_bytes), _stream(stream)),
            "muon_step_batched")
 
 
@@ -421,8 +422,9 @@ def adamw_step_fused(P, G, M, V, hp: AdamWHParams, stream=None, gdt: int | None 
     if gdt is None:
         gdt = _dtype_code(G[0]) if n else MA_F32
     nar = _numel_array(P) if numel is None else (ctypes.c_int64 * max(1, n))(*numel)
+    coef = _clip_ptr("adamw_step_fused", clip, CLIP_HEAD_BYTES, _on_current_gpu)
     _check(lib().adamw_step_fused_clipped(n, _ptr_array(P), _ptr_array(G), int(gdt), _ptr_array(M), _ptr_array(V),
-                                          nar, ctypes.byref(hp), _ptr(clip), _stream(stream)), "adamw_step_fused")
+                                          nar, ctypes.byref(hp), coef, _stream(stream)), "adamw_step_fused")
 
 
 CLIP_BYTES = 16640  # MA_CLIP_BYTES
@@ -447,6 +449,26 @@ def _on_current_gpu(what: str, *tensors) -> None:
             raise MAError(MA_ERR_ARG, f"{what}: tensor on {t.device}, not on the current CUDA device")
 
 
+def _on_gpu(what: str, *tensors) -> None:
+    """Refuse tensors that are not on a GPU."""
+    for t in tensors:
+        if not t.is_cuda:
+            raise MAError(MA_ERR_ARG, f"{what}: tensor on {t.device}, not on a GPU")
+
+
+CLIP_HEAD_BYTES = 16  # norm, coefficient and sum of squares: all that is read of a buffer that is not filled
+
+
+def _clip_ptr(what: str, clip, nbytes: int, on_gpu) -> int:
+    """Address of a clip buffer of which ``nbytes`` are read or written (a plain address, or None, is taken as it is)."""
+    if clip is None or isinstance(clip, int):
+        return _ptr(clip)
+    on_gpu(what, clip)
+    if not clip.is_contiguous() or clip.numel() * clip.element_size() < nbytes:
+        raise MAError(MA_ERR_WORKSPACE, f"{what}: a clip buffer has {CLIP_BYTES} contiguous bytes")
+    return _ptr(clip)
+
+
 def _grad_tables(G):
     """Pointer, dtype and element-count arrays of a list of gradients (contiguous tensors)."""
     n = len(G)
@@ -460,29 +482,29 @@ def ma_grad_norm(G, clip, max_norm: float = math.inf, scale: float = 1.0, stream
     """Global norm of a list of gradients (fp32 or bf16, any mix) into the clip buffer: norm = scale * sqrt(sum g^2)
     and coef = scale * min(1, max_norm / norm), 0 when the norm is not finite. The gradients are left alone:
     adamw_step_fused, muon_step_batched and the plan's steps take them times coef."""
-    _on_current_gpu("ma_grad_norm", clip, *G)
-    _check(lib().ma_grad_norm(*_grad_tables(G), float(scale), float(max_norm), _ptr(clip), _stream(stream)),
-           "ma_grad_norm")
+    _on_current_gpu("ma_grad_norm", *G)
+    buf = _clip_ptr("ma_grad_norm", clip, CLIP_BYTES, _on_current_gpu)
+    _check(lib().ma_grad_norm(*_grad_tables(G), float(scale), float(max_norm), buf, _stream(stream)), "ma_grad_norm")
 
 
 def ma_grad_clip(G, clip, max_norm: float, scale: float = 1.0, stream=None) -> None:
     """ma_grad_norm, then every gradient times coef, in place (zero, whatever it holds, where coef is 0)."""
-    _on_current_gpu("ma_grad_clip", clip, *G)
-    _check(lib().ma_grad_clip(*_grad_tables(G), float(scale), float(max_norm), _ptr(clip), _stream(stream)),
-           "ma_grad_clip")
+    _on_current_gpu("ma_grad_clip", *G)
+    buf = _clip_ptr("ma_grad_clip", clip, CLIP_BYTES, _on_current_gpu)
+    _check(lib().ma_grad_clip(*_grad_tables(G), float(scale), float(max_norm), buf, _stream(stream)), "ma_grad_clip")
 
 
 def ma_clip_finalize(clip, max_norm: float = math.inf, scale: float = 1.0, stream=None) -> None:
     """Norm and coef again from the buffer's sum of squares (after the sums of several ranks were added)."""
-    _on_current_gpu("ma_clip_finalize", clip)
-    _check(lib().ma_clip_finalize(float(scale), float(max_norm), _ptr(clip), _stream(stream)), "ma_clip_finalize")
+    buf = _clip_ptr("ma_clip_finalize", clip, CLIP_HEAD_BYTES, _on_current_gpu)
+    _check(lib().ma_clip_finalize(float(scale), float(max_norm), buf, _stream(stream)), "ma_clip_finalize")
 
 
 def ma_plan_set_clip(plan, clip, max_norm: float = math.inf, scale: float = 1.0, measure: bool = True) -> None:
     """Clip the gradients of the plan's later steps by their global norm, through this buffer (None: off again).
     measure=False: the steps take the coefficient the buffer holds by then, and fill nothing."""
-    _check(lib().ma_plan_set_clip(plan, int(bool(measure)), float(scale), float(max_norm), _ptr(clip)),
-           "ma_plan_set_clip")
+    buf = _clip_ptr("ma_plan_set_clip", clip, CLIP_BYTES if measure else CLIP_HEAD_BYTES, _on_gpu)
+    _check(lib().ma_plan_set_clip(plan, int(bool(measure)), float(scale), float(max_norm), buf), "ma_plan_set_clip")
 
 
 NO_PADDING = -(1 << 63)
