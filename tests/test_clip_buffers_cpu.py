@@ -25,7 +25,7 @@ def as_if_on_gpu(monkeypatch):
 
 
 SHORT = [torch.empty(4), torch.empty(ma.CLIP_BYTES // 4 - 1), torch.empty(ma.CLIP_BYTES // 4, dtype=torch.bfloat16),
-         torch.empty(1).expand(ma.CLIP_BYTES // 4), torch.empty(2, ma.CLIP_BYTES // 4).t()[:, 0]]
+         torch.empty(1).expand(ma.CLIP_BYTES // 4), torch.empty(ma.CLIP_BYTES // 4, 2)[:, 0]]
 FILL = [lambda c, g: ma.ma_grad_norm([g], c), lambda c, g: ma.ma_grad_clip([g], c, 1.0),
         lambda c, g: ma.ma_plan_set_clip(0x1000, c, 1.0)]
 # these read or write the first 16 bytes alone
