@@ -609,6 +609,8 @@ def embedding_grad(ids, grad_rows, grad, scale: float = 1.0, padding: int | None
         if ws_bytes:
             ws = _new(grad, ws_bytes, _torch().uint8, stream)
     else:
+        if not ws.is_contiguous():
+            raise MAError(MA_ERR_WORKSPACE, "embedding_grad: ws must be contiguous")
         ws_bytes = ws.numel() * ws.element_size()
     _check(lib().ma_embed_grad(n, _ptr(ids), idt, V, D, _ptr(y), _dtype_code(grad_rows), ldy, float(scale),
                                NO_PADDING if padding is None else int(padding), int(bool(accumulate)), _ptr(g),
