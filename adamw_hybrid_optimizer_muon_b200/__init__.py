@@ -232,14 +232,30 @@ class _Methods:
         return bytearray(array.array("q", map(_torch().Tensor.numel, xs)))
 
 
+class _Addresses:
+    """The same where torch is not installed: the items are addresses, or have the methods."""
+
+    @staticmethod
+    def pointers(xs):
+        return bytearray(array.array("Q", map(_ptr, xs)))
+
+    @staticmethod
+    def numels(xs):
+        return bytearray(array.array("q", [int(x.numel()) for x in xs]))
+
+
 _MARSHAL = None
 
 
 def _marshal():
-    """The extension module that reads lists of tensors (lib/_marshal.so), or the methods in its place."""
+    """The extension module that reads lists of tensors (lib/_marshal.so), or what stands in its place."""
     global _MARSHAL
     if _MARSHAL is None:
-        _torch()  # whose libraries it is linked to
+        try:
+            _torch()  # whose libraries it is linked to
+        except ImportError:
+            _MARSHAL = _Addresses
+            return _MARSHAL
         path = os.path.join(os.path.dirname(LIB_PATH), "_marshal.so")
         try:
             loader = importlib.machinery.ExtensionFileLoader("_marshal", path)
