@@ -15,6 +15,7 @@ import importlib.util
 import ctypes
 import math
 import os
+import sysconfig
 from typing import Sequence
 
 __all__ = [
@@ -244,25 +245,31 @@ class _Addresses:
         return bytearray(array.array("q", [int(x.numel()) for x in xs]))
 
 
+def _marshal_path(torch) -> str:
+    """Where the extension module for this Python and this torch is, or would be. It was compiled with the layout of
+    that torch's tensors, which another torch need not share although it has every symbol: so the name tells."""
+    abi = sysconfig.get_config_var("SOABI")
+    return os.path.join(os.path.dirname(LIB_PATH), f"_marshal.{abi}.torch-{torch.__version__}.so")
+
+
 _MARSHAL = None
 
 
 def _marshal():
-    """The extension module that reads lists of tensors (lib/_marshal.so), or what stands in its place."""
+    """The extension module that reads lists of tensors, or what stands in its place."""
     global _MARSHAL
     if _MARSHAL is None:
         try:
-            _torch()  # whose libraries it is linked to
+            path = _marshal_path(_torch())  # whose libraries it is linked to
         except ImportError:
             _MARSHAL = _Addresses
             return _MARSHAL
-        path = os.path.join(os.path.dirname(LIB_PATH), "_marshal.so")
         try:
             loader = importlib.machinery.ExtensionFileLoader("_marshal", path)
             module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("_marshal", path, loader=loader))
             loader.exec_module(module)
             _MARSHAL = module
-        except ImportError:  # not built, or against another torch
+        except ImportError:  # not built for this Python and torch
             _MARSHAL = _Methods
     return _MARSHAL
 

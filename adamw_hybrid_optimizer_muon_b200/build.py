@@ -9,8 +9,8 @@ index against the extent of its buffer (a failed check records MA_ERR_BOUNDS
 and skips the access) and otherwise computes the same bits. Each object is
 rebuilt only when a source or header is newer than it; the objects compile in
 parallel. nvcc cross-compiles, so no GPU is needed. ``csrc/marshal.cpp`` becomes
-``lib/_marshal.so``, a Python extension module built against the installed torch;
-the libraries do not need it, and where it cannot be built there is a warning.
+a Python extension module built against the installed torch (its name in ``lib/``
+has the versions of Python and torch); the libraries do not need it, and where it cannot be built there is a warning.
 """
 from __future__ import annotations
 
@@ -22,13 +22,14 @@ import subprocess
 import sys
 import sysconfig
 
+from . import _marshal_path
+
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB_DIR = os.path.join(HERE, "lib")
 LIB = os.path.join(LIB_DIR, "libmuonadamw.so")
-MARSHAL = os.path.join(LIB_DIR, "_marshal.so")
 LIB_DEBUG = os.path.join(LIB_DIR, "libmuonadamw_debug.so")
 VARIANTS = (("release", LIB, []), ("debug", LIB_DEBUG, ["-DMA_DEBUG"]))
 
@@ -53,17 +54,18 @@ def _build_marshal(verbose: bool, force: bool) -> None:
     """The extension module that reads lists of tensors. The binding does without it, more slowly: what goes wrong
     here is reported and not raised."""
     src = os.path.join(CSRC, "marshal.cpp")
-    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= os.path.getmtime(src):
-        return
     try:
         import torch
     except ImportError:
         sys.stderr.write("marshal.cpp not built: torch cannot be imported\n")
         return
+    out = _marshal_path(torch)
+    if not force and os.path.exists(out) and os.path.getmtime(out) >= os.path.getmtime(src):
+        return
     base = os.path.dirname(torch.__file__)
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-shared", "-fPIC", "-w",
            "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(base, "include"),
-           "-I" + os.path.join(base, "include", "torch", "csrc", "api", "include"), src, "-o", MARSHAL,
+           "-I" + os.path.join(base, "include", "torch", "csrc", "api", "include"), src, "-o", out,
            "-L" + os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
     try:
         res = subprocess.run(cmd, capture_output=True, text=True)

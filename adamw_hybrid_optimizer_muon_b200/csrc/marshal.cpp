@@ -2,8 +2,9 @@
 // the C entry points take: through Python's methods a tensor costs 60 ns a
 // value, here about 2.
 //
-// A Python extension module, built against the installed torch; the binding
-// goes through the methods where it is not there. Both functions raise
+// A Python extension module, built against the installed torch and loaded with
+// that torch and that Python alone (the versions are in the file's name); the
+// binding goes through the methods where it is not there. Both functions raise
 // TypeError when an item is not a plain tensor (the binding then does it the
 // long way, with that way's errors).
 #define PY_SSIZE_T_CLEAN
