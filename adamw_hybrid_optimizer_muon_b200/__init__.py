@@ -641,6 +641,30 @@ def embedding_grad(ids, grad_rows, grad, scale: float = 1.0, padding: int | None
     return grad
 
 
+_LAST_SUM = {}  # per device: stream, backward pass and capture of the last sum into a gradient buffer, and its event
+
+
+def _sum_in_turn(device, add) -> None:
+    """add(), a sum into a gradient buffer within a backward pass, after the one before it.
+
+    Autograd runs each lookup's backward on the stream of its forward, and joins streams along the edges of the
+    graph; two lookups that add to one buffer have no edge between them. So each sum waits for the last one on this
+    device when that ran on another stream (whatever its buffer: two views may be one). An event and a wait belong
+    to one capture or to none: a captured sum waits for those of its own backward pass, which is captured whole, an
+    eager one for any eager one."""
+    cuda = _torch().cuda
+    stream, captured = cuda.current_stream(device), cuda.is_current_stream_capturing()
+    task = _torch()._C._current_graph_task_id()
+    if device in _LAST_SUM:
+        last_stream, last_task, last_captured, event = _LAST_SUM[device]
+        if stream != last_stream and (task == last_task or not (captured or last_captured)):
+            stream.wait_event(event)
+    add()
+    event = cuda.Event()
+    event.record(stream)
+    _LAST_SUM[device] = stream, task, captured, event
+
+
 _EMBEDDING = None
 
 
@@ -666,7 +690,7 @@ def _embedding_function():
             scale, padding, grad, shape, dtype, device = ctx.args
             dy = dy.contiguous()
             if grad is not None:
-                embedding_grad(ids, dy, grad, scale, padding, accumulate=True)
+                _sum_in_turn(grad.device, lambda: embedding_grad(ids, dy, grad, scale, padding, accumulate=True))
                 return (None,) * 7
             out = torch.empty(shape, dtype=dtype, device=device)
             return None, embedding_grad(ids, dy, out, scale, padding), None, None, None, None, None
@@ -682,6 +706,10 @@ def embedding(ids, table, scale: float = 1.0, padding: int | None = None, dtype=
     grad) that backward adds the gradient to, in place of returning one: the buffer the optimizer reads can
     then be filled over several micro-batches, and no table-sized gradient is
     made and added. The caller zeroes it, and it is complete when backward is.
+    Lookups of one pass may run on several streams: their sums into buffers are
+    ordered. What else writes to the buffer in that pass (the table's own
+    ``.grad``, say, when the table is used elsewhere too) has to be on the same
+    stream as they are.
 
     A backward pass captured into a CUDA graph: with ``grad``, at any time;
     without, as with any operator of torch, only while no output of an earlier
