@@ -503,7 +503,8 @@ def _grad_tables(G):
 
 def ma_grad_norm(G, clip, max_norm: float = math.inf, scale: float = 1.0, stream=None) -> None:
     """Global norm of a list of gradients (fp32 or bf16, any mix) into the clip buffer: norm = scale * sqrt(sum g^2)
-    and coef = scale * min(1, max_norm / norm), 0 when the norm is not finite. The gradients are left alone:
+    and coef = scale * min(1, max_norm / norm), 0 when the sum of squares (in fp64) is not finite. A norm beyond fp32
+    reads infinite, with the coef of its fp64 value. The gradients are left alone:
     adamw_step_fused, muon_step_batched and the plan's steps take them times coef."""
     _on_current_gpu("ma_grad_norm", *G)
     buf = _clip_ptr("ma_grad_norm", clip, CLIP_BYTES, _on_current_gpu)
@@ -1067,17 +1068,27 @@ class MuonAdamW:
     @property
     def grad_norm(self):
         """Global gradient norm (times grad_scale) of the last step that had one, as a 0-d device tensor that the
-        next such step overwrites. Infinite or NaN: that step took every gradient as zero."""
+        next such step overwrites. NaN or infinite where a gradient was (that step took every gradient as zero), and
+        infinite too where finite gradients have a norm beyond fp32 (that step clipped them): grad_coef tells."""
         if self._clip is None:
             raise RuntimeError("no step with max_norm or grad_scale yet")
         return self._clip[0]
 
+    @property
+    def grad_coef(self):
+        """What the last step with max_norm or grad_scale multiplied the gradients by, as a 0-d device tensor that
+        the next such step overwrites. 0 where max_norm is above it: a gradient was not finite, and that step took
+        every one as zero."""
+        if self._clip is None:
+            raise RuntimeError("no step with max_norm or grad_scale yet")
+        return self._clip[1]
+
     def step(self, grads=None, stream=None, graph: bool = False, max_norm: float | None = None,
              grad_scale: float = 1.0) -> None:
         """One step. max_norm: clip the gradients to this global norm; grad_scale: what they have to be multiplied by
-        first (1 / loss scale). Both are applied as the step reads the gradients, which stay as they are; a norm that
-        is not finite makes it a step with zero gradients (see grad_norm). graph=True replays the step from a CUDA graph that the plan
-        captures on first use (same results; one launch instead of one per kernel).
+        first (1 / loss scale). Both are applied as the step reads the gradients, which stay as they are; a gradient
+        that is not finite makes it a step with zero gradients (grad_coef is then 0). graph=True replays the step from
+        a CUDA graph that the plan captures on first use (same results; one launch instead of one per kernel).
         A plan, and with it the graph, belongs to one set of gradient buffers:
         keep them at fixed addresses (as persistent ``.grad`` tensors are)."""
         if grads is None:

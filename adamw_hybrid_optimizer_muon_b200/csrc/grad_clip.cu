@@ -4,8 +4,10 @@
 //   coef = scale * min(1, max_norm / N)          g <- coef * g (in place), or the
 //                                                AdamW and momentum passes take
 //                                                coef * g as they read g
-// A norm that is not finite gives coef = 0, and a gradient times a zero coef is
-// taken as zero, whatever it holds: no NaN or infinity reaches a parameter.
+// A sum of squares that is not finite gives coef = 0, and a gradient times a
+// zero coef is taken as zero, whatever it holds: no NaN or infinity reaches a
+// parameter. (The sum is fp64: finite gradients whose norm is beyond fp32 are
+// clipped like others, though the norm, a float, reads infinite.)
 //
 // Bound by HBM: the norm reads every gradient once; clipping in place reads and
 // writes each once more. One launch covers up to kClipMaxTensors tensors; the

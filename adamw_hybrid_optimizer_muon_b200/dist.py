@@ -231,11 +231,21 @@ class DistMuonAdamW:
     @property
     def grad_norm(self) -> torch.Tensor:
         """Global norm of the averaged gradients (times grad_scale) of the last step that had one, the same on every
-        rank: a 0-d tensor on the device that the next such step overwrites. Infinite or NaN: that step took every
-        gradient as zero."""
+        rank: a 0-d tensor on the device that the next such step overwrites. NaN or infinite where a gradient was (that
+        step took every gradient as zero), and infinite too where finite gradients have a norm beyond fp32 (that step
+        clipped them): grad_coef tells."""
         if self._clip is None:
             raise RuntimeError("no step with max_norm or grad_scale yet")
         return self._clip[0]
+
+    @property
+    def grad_coef(self) -> torch.Tensor:
+        """What the last step with max_norm or grad_scale multiplied the averaged gradients by, the same on every
+        rank: a 0-d tensor on the device that the next such step overwrites. 0 where max_norm is above it: a gradient
+        was not finite, and that step took every one as zero."""
+        if self._clip is None:
+            raise RuntimeError("no step with max_norm or grad_scale yet")
+        return self._clip[1]
 
     def step(self, max_norm: float | None = None, grad_scale: float = 1.0) -> None:
         """One data-parallel step: reduce-scatter, local update, all-gather (all asynchronous on the device).

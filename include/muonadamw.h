@@ -303,9 +303,12 @@ int adamw_step_fused(int n, float* const* P, const void* const* G, int gdt, floa
  * measures and scales without clipping. When the sum of squares is not finite
  * (an infinity or a NaN among the gradients), coef is 0; a gradient times a
  * coef of 0 is 0 whatever it holds, so that step goes on as with zero
- * gradients, and norm tells. Squares are summed in fp64 beyond 64 values, and
- * in fp64 throughout where fp32 would overflow or lose them; the order is
- * fixed, so the same call on the same GPU model gives the same bits.
+ * gradients: a coef of 0 under a max_norm above 0 tells. (norm is a float: it
+ * reads infinite for finite gradients whose norm is beyond fp32 as well, while
+ * coef is formed from the fp64 sum and clips them.) Squares are summed in fp64
+ * beyond 64 values, and in fp64 throughout where fp32 would overflow or lose
+ * them; the order is fixed, so the same call on the same GPU model gives the
+ * same bits.
  *
  * clip: device buffer of MA_CLIP_BYTES, 256-byte aligned, owned by the caller:
  * bytes 0..3 norm (float, N), 4..7 coef (float), 8..15 the sum of squares of
