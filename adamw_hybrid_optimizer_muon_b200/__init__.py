@@ -232,6 +232,10 @@ class _Methods:
     def numels(xs):
         return bytearray(array.array("q", map(_torch().Tensor.numel, xs)))
 
+    @classmethod
+    def unchanged(cls, xs, ptrs, counts):
+        return cls.pointers(xs) == ptrs and cls.numels(xs) == counts
+
 
 class _Addresses:
     """The same where torch is not installed: the items are addresses, or have the methods."""
@@ -919,29 +923,44 @@ class GradClip:
     """Global norm and clipping of a fixed list of gradients (contiguous fp32 or bf16 tensors on one GPU).
 
     Keeps the pointer tables, so that a call costs a few microseconds of host
-    time, and the clip ``buffer`` that the steps take. The gradients stay at
-    their addresses (as persistent ``.grad`` tensors do). Calls that overlap on
-    the GPU need an object each.
+    time, and the clip ``buffer`` that the steps take. It clips the tensors it
+    was given, wherever their memory is by then, and keeps them alive: they
+    have to stay the parameters' gradients. After ``zero_grad()`` they are not,
+    since that drops them (``set_to_none=True`` is torch's default); zero them
+    in place (``set_to_none=False``), or make another object. Calls that
+    overlap on the GPU need an object each.
     """
 
     def __init__(self, grads):
         self.grads = list(grads)
-        _on_current_gpu("GradClip", *self.grads)
-        self._tables = _grad_tables(self.grads)
-        self._args = (self._tables[0], *[ctypes.addressof(a) for a in self._tables[1:]])
+        self._read_gradients()
         self.buffer = clip_buffer()
         self._norm = self.buffer[0]
         self._ptr = _ptr(self.buffer)
+        self._device = self.buffer.get_device()
+
+    def _read_gradients(self):
+        _on_current_gpu("GradClip", *self.grads)
+        self._tables = _grad_tables(self.grads)
+        self._args = (self._tables[0], *[ctypes.addressof(a) for a in self._tables[1:]])
+        self._read = (_marshal().pointers(self.grads), _marshal().numels(self.grads))
+
+    def _ready(self, what: str):
+        """Before a call: the device is the buffer's, and the tables are those of the gradients as they are."""
+        if _torch()._C._cuda_getDevice() != self._device:
+            _on_current_gpu(what, self.buffer)
+        if not _marshal().unchanged(self.grads, *self._read):
+            self._read_gradients()
 
     def norm(self, max_norm: float = math.inf, scale: float = 1.0, stream=None):
         """Fill ``buffer``; the norm (times scale) as a 0-d view of it, on the device. The next call overwrites it."""
-        _on_current_gpu("GradClip.norm", self.buffer)
+        self._ready("GradClip.norm")
         _check(lib().ma_grad_norm(*self._args, scale, max_norm, self._ptr, _stream(stream)), "ma_grad_norm")
         return self._norm
 
     def clip(self, max_norm: float, scale: float = 1.0, stream=None):
         """Scale and clip the gradients in place; returns their norm before clipping, as :meth:`norm` does."""
-        _on_current_gpu("GradClip.clip", self.buffer)
+        self._ready("GradClip.clip")
         _check(lib().ma_grad_clip(*self._args, scale, max_norm, self._ptr, _stream(stream)), "ma_grad_clip")
         return self._norm
 
