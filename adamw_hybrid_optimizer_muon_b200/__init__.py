@@ -741,7 +741,7 @@ def qk_max_logit(q, k, scale: float | None = None, causal: bool = True, offsets=
     end to end, none longer than ``max_len``; default: all tokens). k: the same
     with a number of heads that divides q's. dim: a multiple of 8 up to 256;
     strides multiples of 8. scale: default dim ** -0.5. ``accumulate`` takes the
-    maximum with what ``out`` holds. Without a visible pair: -inf; a NaN logit: NaN."""
+    maximum with what ``out`` holds. Without a visible pair: -inf; a NaN logit, or one that ``out`` holds: NaN."""
     torch = _torch()
     _on_current_gpu("qk_max_logit", q, k, offsets, out)
     nd = 3 if offsets is not None else 4

@@ -105,6 +105,7 @@ struct QkLaunch {
     const int32_t* offsets;  // packed: first token of each sequence and the end; NULL: sequences of `len` tokens
     int32_t seqs, len, total;  // len: tokens per sequence (packed: the longest); total: tokens of a packed batch
     int32_t heads, kv;
+    int32_t given;  // `out` holds values of the caller's (else -infinity)
     float scale;
     float* out;
     long long wait_limit_ns;
@@ -343,8 +344,12 @@ __device__ __forceinline__ void reduce32_masked(const uint32_t (&r)[32], int n, 
 
 // Floats in order as the bits that the integer maximum and minimum order;
 // works from an initial -infinity. A NaN (0x7fffffff) is above everything.
-__device__ __forceinline__ void atomic_max_float(float* p, float v) {
+// Where the caller's values are there (`given`), a NaN among them may have its
+// sign set and be below everything: the first to come, whichever that is, still
+// finds it and puts the other one in its place, and so does everyone after.
+__device__ __forceinline__ void atomic_max_float(float* p, float v, bool given) {
     v += 0.f;  // -0 to +0
+    if (given && isnan(__ldcg(p))) v = __int_as_float(0x7fffffff);
     if (v < 0.f) atomicMin(reinterpret_cast<unsigned*>(p), __float_as_uint(v));
     else atomicMax(reinterpret_cast<int*>(p), (int)(isnan(v) ? 0x7fffffffu : __float_as_uint(v)));
 }
@@ -626,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1) qk_max_kernel(const __grid_consta
             float v = max_nan(max_nan(m[0], m[1]), max_nan(m[2], m[3]));
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) v = max_nan(v, __shfl_xor_sync(0xffffffffu, v, o));
-            if (lane == 0 && v != -INFINITY) atomic_max_float(&L.out[g.h], v * L.scale);
+            if (lane == 0 && v != -INFINITY) atomic_max_float(&L.out[g.h], v * L.scale, L.given);
         }
     }
     __syncwarp();
@@ -855,6 +860,7 @@ int qk_max(int64_t seqs, int64_t len, int64_t total, int heads, int kv_heads, in
         L.total = (int)total;
         L.heads = heads;
         L.kv = kv_heads;
+        L.given = accumulate;
         L.scale = scale;
         L.out = out;
         L.wait_limit_ns = host_wait_limit_ns();
