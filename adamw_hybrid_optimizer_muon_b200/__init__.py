@@ -780,7 +780,11 @@ def qk_clip(wq, wk, max_logit, tau: float = 100.0, alpha: float = 0.5, kv_heads:
     cols, wk: (kv_heads * k_rows) x cols, fp32, contiguous (kv_heads: default heads). The query weights take the
     factor to the power alpha, the key weights the rest; a key head shared by several query heads takes what the
     one furthest over needs, and its query heads' weights make up for it, so that each head's logits scale by its
-    own factor. Heads within tau, or whose maximum is not finite, are not touched."""
+    own factor: those of heads within tau, or whose maximum is not finite, by one. The weights of such a head are not
+    touched unless it shares its key head with one over tau (its query weights then grow by what its keys lose).
+
+    Weights replicated over data-parallel ranks: each rank has the maximum of its own batch, and the ranks' weights
+    part unless all clip by the same one. Reduce it first: ``dist.all_reduce(max_logit, dist.ReduceOp.MAX)``."""
     torch = _torch()
     _on_current_gpu("qk_clip", wq, wk, max_logit)
     for t in (wq, wk, max_logit):

@@ -408,7 +408,9 @@ int ma_qk_max_logit(int64_t seqs, int64_t len, int64_t total, int heads, int kv_
  * so that head h's logits scale by g_h; W_q's factor is g_h^alpha where no key
  * head is shared. wq: heads * q_rows x cols, wk: kv_heads * k_rows x cols,
  * device, fp32, row-major, head after head. Rows whose factor is 1 are not
- * touched. 0 <= alpha <= 1 (1/2: shared evenly). At most 2048 heads in all. */
+ * touched. 0 <= alpha <= 1 (1/2: shared evenly). At most 2048 heads in all.
+ * Weights replicated over data-parallel ranks need the maximum over all ranks'
+ * batches: reduce max_logit (MAX) first, or the replicas part. */
 int ma_qk_clip(int heads, int kv_heads, int64_t q_rows, int64_t k_rows, int64_t cols, float* wq, float* wk,
                const float* max_logit, float tau, float alpha, void* stream);
 
