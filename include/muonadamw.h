@@ -53,9 +53,10 @@ typedef enum {
     MA_ERR_CUDA = 7,        /* a CUDA runtime call failed                         */
     MA_ERR_TIMEOUT = 8,     /* a device-side bounded wait ran out (status word)   */
     MA_ERR_ARG = 9,         /* a hyperparameter is out of its domain              */
-    MA_ERR_BOUNDS = 10      /* a token id outside the embedding table; in debug   */
-                            /* builds also a guarded device index outside its     */
-                            /* buffer, the access skipped (status word)           */
+    MA_ERR_BOUNDS = 10      /* a token id outside the embedding table, or packed  */
+                            /* sequence offsets that do not fit the batch; in     */
+                            /* debug builds also a guarded device index outside   */
+                            /* its buffer, the access skipped (status word)       */
 } ma_status_t;
 
 typedef enum { MA_F32 = 0, MA_BF16 = 1, MA_I32 = 2, MA_I64 = 3 } ma_dtype_t; /* integers: token ids only */
@@ -140,6 +141,8 @@ typedef struct ma_plan ma_plan_t;
 
 /* ---------------------------------------------------------------- host-only */
 
+/* A few words for a status. (Those for MA_ERR_BOUNDS name the debug builds'
+ * guarded index alone; see the enum for what else it stands for.) */
 const char* ma_status_string(int status);
 int ma_version(void);
 
@@ -543,7 +546,8 @@ int ma_device_status(void* stream, int reset);
  * steps were launched on), then read and clear the status word of the current
  * device, as ma_device_status(stream, 1) does. Returns MA_ERR_NULL for a NULL
  * plan, MA_ERR_CUDA when the device cannot be reached, else MA_OK or the
- * first device-side error (MA_ERR_TIMEOUT) since the last read. */
+ * first device-side error on the device since the last read (of a step
+ * MA_ERR_TIMEOUT). */
 int ma_plan_status(ma_plan_t* plan, void* stream);
 
 /* Enqueue on `stream` a copy of the current device's status word into
