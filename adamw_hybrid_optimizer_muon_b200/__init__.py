@@ -705,7 +705,8 @@ def _embedding_function():
 
 
 def embedding(ids, table, scale: float = 1.0, padding: int | None = None, dtype=None, grad=None):
-    """embedding_lookup with a gradient for the table (embedding_grad; not differentiable twice).
+    """embedding_lookup with a gradient for the table (embedding_grad; not differentiable twice, and without a forward
+    mode, vmap or the transforms of torch.func).
 
     ``grad``: a fp32 or bf16 buffer of the shape of the table (which requires
     grad) that backward adds the gradient to, in place of returning one: the buffer the optimizer reads can
@@ -714,7 +715,10 @@ def embedding(ids, table, scale: float = 1.0, padding: int | None = None, dtype=
     Lookups of one pass may run on several streams: their sums into buffers are
     ordered. What else writes to the buffer in that pass (the table's own
     ``.grad``, say, when the table is used elsewhere too) has to be on the same
-    stream as they are.
+    stream as they are. Autograd does not see this gradient: hooks on the table
+    (register_hook, register_post_accumulate_grad_hook, a wrapper that reduces
+    gradients in one) do not run for it, and torch.autograd.grad finds no path
+    to the table.
 
     A backward pass captured into a CUDA graph: with ``grad``, at any time;
     without, as with any operator of torch, only while no output of an earlier
