@@ -489,11 +489,11 @@ CLIP_HEAD_BYTES = 16  # norm, coefficient and sum of squares: all that is read o
 def _clip_ptr(what: str, clip, nbytes: int, on_gpu) -> int:
     """Address of a clip buffer of which ``nbytes`` are read or written (a plain address, or None, is taken as it is)."""
     if clip is None or isinstance(clip, int):
-        return _ptr(clip)
+        return clip or 0
     on_gpu(what, clip)
-    if not clip.is_contiguous() or clip.numel() * clip.element_size() < nbytes:
+    if clip.nbytes < nbytes or not clip.is_contiguous():
         raise MAError(MA_ERR_WORKSPACE, f"{what}: a clip buffer has {CLIP_BYTES} contiguous bytes")
-    return _ptr(clip)
+    return clip.data_ptr()
 
 
 def _grad_tables(G):
@@ -951,13 +951,15 @@ class GradClip:
         _on_current_gpu("GradClip", *self.grads)
         self._tables = _grad_tables(self.grads)
         self._args = (self._tables[0], *[ctypes.addressof(a) for a in self._tables[1:]])
-        self._read = (_marshal().pointers(self.grads), _marshal().numels(self.grads))
+        self._read = (self.grads, _marshal().pointers(self.grads), _marshal().numels(self.grads))
+        self._unchanged = _marshal().unchanged
+        self._get_device = _torch()._C._cuda_getDevice
 
     def _ready(self, what: str):
         """Before a call: the device is the buffer's, and the tables are those of the gradients as they are."""
-        if _torch()._C._cuda_getDevice() != self._device:
+        if self._get_device() != self._device:
             _on_current_gpu(what, self.buffer)
-        if not _marshal().unchanged(self.grads, *self._read):
+        if not self._unchanged(*self._read):
             self._read_gradients()
 
     def norm(self, max_norm: float = math.inf, scale: float = 1.0, stream=None):
