@@ -646,28 +646,51 @@ def embedding_grad(ids, grad_rows, grad, scale: float = 1.0, padding: int | None
     return grad
 
 
-_LAST_SUM = {}  # per device: stream, backward pass and capture of the last sum into a gradient buffer, and its event
+_SUM_STREAMS = {}  # per device: stream objects, by handle, of lookups whose gradients go to buffers
+_LAST_SUM = {}     # per device: stream, backward pass and capture of the last such sum, and the event after it
 
 
-def _sum_in_turn(device, add) -> None:
-    """add(), a sum into a gradient buffer within a backward pass, after the one before it.
+def _sum_stream(index: int) -> int:
+    """The handle of device ``index``'s current stream, which is from now on among those of lookups into buffers."""
+    stream = _torch()._C._cuda_getCurrentRawStream(index)
+    known = _SUM_STREAMS.get(index)
+    if known is None or stream not in known:
+        _SUM_STREAMS[index] = {**(known or {}), stream: _torch().cuda.ExternalStream(stream, device=index)}
+    return stream
+
+
+def _sum_in_turn(index: int, add) -> None:
+    """add(), a sum into a gradient buffer of device ``index`` within a backward pass, after the one before it.
 
     Autograd runs each lookup's backward on the stream of its forward, and joins streams along the edges of the
     graph; two lookups that add to one buffer have no edge between them. So each sum waits for the last one on this
     device when that ran on another stream (whatever its buffer: two views may be one). An event and a wait belong
     to one capture or to none: a captured sum waits for those of its own backward pass, which is captured whole, an
-    eager one for any eager one."""
-    cuda = _torch().cuda
-    stream, captured = cuda.current_stream(device), cuda.is_current_stream_capturing()
-    task = _torch()._C._current_graph_task_id()
-    if device in _LAST_SUM:
-        last_stream, last_task, last_captured, event = _LAST_SUM[device]
-        if stream != last_stream and (task == last_task or not (captured or last_captured)):
-            stream.wait_event(event)
+    eager one for any eager one.
+
+    While all lookups were on one stream there is nothing to wait for, and no event is recorded (7 us of the host's
+    time a sum in a backward pass). A sum from that time is waited for by what is left: its stream as it is then,
+    where the pass is the same, so that the stream is there, else the device."""
+    torch = _torch()
+    stream, task = _sum_stream(index), torch._C._current_graph_task_id()
+    known, last = _SUM_STREAMS[index], _LAST_SUM.get(index)
+    if len(known) == 1:
+        add()
+        _LAST_SUM[index] = stream, task, False, None
+        return
+    captured = torch._C._cuda_isCurrentStreamCapturing()
+    if last is not None and stream != last[0]:
+        if last[3] is not None:
+            if task == last[1] or not (captured or last[2]):
+                known[stream].wait_event(last[3])
+        elif task == last[1]:
+            known[stream].wait_stream(known[last[0]])
+        elif not captured:
+            torch.cuda.synchronize(index)
     add()
-    event = cuda.Event()
-    event.record(stream)
-    _LAST_SUM[device] = stream, task, captured, event
+    event = torch.cuda.Event() if captured or last is None or last[2] or last[3] is None else last[3]
+    event.record(known[stream])
+    _LAST_SUM[index] = stream, task, captured, event
 
 
 _EMBEDDING = None
@@ -695,7 +718,8 @@ def _embedding_function():
             scale, padding, grad, shape, dtype, device = ctx.args
             dy = dy.contiguous()
             if grad is not None:
-                _sum_in_turn(grad.device, lambda: embedding_grad(ids, dy, grad, scale, padding, accumulate=True))
+                _sum_in_turn(grad.get_device(),
+                             lambda: embedding_grad(ids, dy, grad, scale, padding, accumulate=True))
                 return (None,) * 7
             out = torch.empty(shape, dtype=dtype, device=device)
             return None, embedding_grad(ids, dy, out, scale, padding), None, None, None, None, None
@@ -730,6 +754,8 @@ def embedding(ids, table, scale: float = 1.0, padding: int | None = None, dtype=
     # Autograd calls backward for a leaf of this call alone: torch binds a leaf to the stream of its first use, and
     # the table's would tie a captured pass to the stream of an eager one.
     torch = _torch()
+    if table.is_cuda:
+        _sum_stream(table.get_device())
     needed = table.requires_grad and torch.is_grad_enabled()
     anchor = torch.empty(0, device=table.device, requires_grad=True) if needed else None
     return _embedding_function().apply(ids, table.detach(), float(scale), padding, dtype, grad, anchor)

@@ -16,6 +16,9 @@ class Stream:
     def wait_event(self, event):
         LOG.append(("wait", self.name, event.after))
 
+    def wait_stream(self, other):
+        LOG.append(("wait for all of", self.name, other.name))
+
 
 class Event:
     after = None
@@ -23,8 +26,9 @@ class Event:
     def __init__(self, **kw):
         pass
 
-    def record(self, stream=None):
-        self.after = (stream or torch.cuda.current_stream()).name, sum(e[0] == "add" for e in LOG)
+    def record(self, stream):
+        LOG.append(("event",))
+        self.after = stream.name, sum(e[0] == "add" for e in LOG)
 
 
 @pytest.fixture
@@ -45,14 +49,19 @@ def fake(monkeypatch):
 
     monkeypatch.setattr(ma, "embedding_lookup", lookup)
     monkeypatch.setattr(ma, "embedding_grad", grad)
-    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: (here["names"] or [Stream("end")])[0])
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: here["names"][0].name)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: Stream(handle))
     monkeypatch.setattr(torch.cuda, "Event", Event)
-    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: bool(here["captured"] and here["captured"][0]))
-    if hasattr(ma, "_LAST_SUM"):
-        monkeypatch.setattr(ma, "_LAST_SUM", {})
+    monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: bool(here["captured"] and here["captured"][0]))
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda index=None: LOG.append(("synchronize",)))
+    monkeypatch.setattr(ma, "_LAST_SUM", {})
+    monkeypatch.setattr(ma, "_SUM_STREAMS", {})
     streams = {}
 
-    def use(names, captured=()):
+    def use(names, captured=(), known=None):
+        """known: the streams that lookups ran on before the backward pass (by default those of the sums)."""
+        for n in names if known is None else known:
+            ma._SUM_STREAMS.setdefault(-1, {}).setdefault(n, Stream(n))  # -1: a host tensor's device
         here["names"] = [streams.setdefault(n, Stream(n)) for n in names]
         here["captured"] = list(captured)
 
@@ -72,13 +81,35 @@ def test_sums_on_two_streams_wait_for_one_another(fake):
     fake("aba")
     buf = passes(3)
     assert buf[3].tolist() == [6.0] * 4
-    assert LOG == [("add", "a"), ("wait", "b", ("a", 1)), ("add", "b"), ("wait", "a", ("b", 2)), ("add", "a")]
+    assert [e for e in LOG if e[0] != "event"] == [("add", "a"), ("wait", "b", ("a", 1)), ("add", "b"),
+                                                   ("wait", "a", ("b", 2)), ("add", "a")]
 
 
-def test_sums_on_one_stream_wait_for_nothing(fake):
+def test_sums_on_one_stream_wait_for_nothing_and_record_nothing(fake):
     fake("aaaa")
     passes(2, calls=2)
-    assert [e for e in LOG if e[0] == "wait"] == []
+    assert LOG == [("add", "a")] * 4
+
+
+def test_the_first_sum_on_a_second_stream_within_a_pass(fake):
+    # a stream that no lookup was on before the backward pass (made within it): the sum before it has no event
+    fake("abab", known="a")
+    passes(4)
+    assert [e for e in LOG if e[0] != "event"] == [
+        ("add", "a"), ("wait for all of", "b", "a"), ("add", "b"), ("wait", "a", ("b", 2)), ("add", "a"),
+        ("wait", "b", ("a", 3)), ("add", "b")]
+
+
+def test_the_first_sum_on_a_second_stream_in_a_later_pass(fake):
+    fake("aab", known="a")
+    passes(1, calls=3)
+    assert [e for e in LOG if e[0] != "event"] == [("add", "a"), ("add", "a"), ("synchronize",), ("add", "b")]
+
+
+def test_the_first_captured_sum_waits_for_no_eager_one(fake):
+    fake("ab", [False, True], known="a")
+    passes(1, calls=2)
+    assert [e for e in LOG if e[0] != "event"] == [("add", "a"), ("add", "b")]
 
 
 def test_a_later_backward_pass_waits_too(fake):
