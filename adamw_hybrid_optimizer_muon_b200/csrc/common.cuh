@@ -1,7 +1,8 @@
 // Device-side helpers shared by the MuonAdamW kernels (sm_100a only).
 //
-// * A per-device status word: kernels record the first error (today only
-//   MA_ERR_TIMEOUT from a bounded wait) and never trap.
+// * A per-device status word: kernels record the first error (MA_ERR_TIMEOUT
+//   from a bounded wait, MA_ERR_BOUNDS from a token id, a sequence offset or, in
+//   debug builds, a guarded index that does not fit) and never trap.
 // * Bounded mbarrier waits: every spin has a limit measured on %globaltimer,
 //   after which the waiter records MA_ERR_TIMEOUT, raises a block-local abort
 //   flag and returns false, so its block can wind down and exit.
