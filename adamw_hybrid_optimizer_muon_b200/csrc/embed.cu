@@ -33,8 +33,8 @@
 // rows have tokens on (a bit per row) writes a share beside its own work, the
 // sums the rest.
 //
-// Measured, bf16: 8192 tokens x 4096 into 32,000 rows 72 us, of which the 262 MB
-// written take 61 at the 4.3 TB/s that plain stores reach on this GPU; 131,072 x
+// Measured, bf16: 8192 tokens x 4096 into 32,000 rows 72 us, where the zeros of
+// the same table without a token take 49 (262 MB at 5.3 TB/s); 131,072 x
 // 1280 of a skewed distribution into 65,536 rows 129 us for 503 MB. Rows that are
 // not whole 16-byte vectors go by two elements or by one, and issue bounds them:
 // uniform tokens of 1282 columns 190 us and of 1281 columns 227, of 1280 115.
@@ -968,7 +968,8 @@ struct GradLayout {
 // skewed distribution 135 us (169), all the same token 161 (222); 1,000,000 x
 // 128 skewed 162 (193), all the same token 301 (901). Sixteen warps, against six
 // blocks alone: 20,000 x 64 skewed 35.5 (38.7), 1,000,000 x 128 162 (185), all
-// the same token 301 (176).
+// the same token 301 (176). (148 as a constant: the workspace, whose size is
+// asked for without a device, depends on the tile.)
 int sum_tile(int64_t n, int64_t dim) {
     const int64_t warps = (dim + 255) / 256, blocks = (warps + 7) / 8;  // of a row, 8 elements to a thread
     int s = kMaxSumTile;
@@ -1169,6 +1170,8 @@ int lookup(int64_t n, const void* ids, int idt, int64_t rows, int64_t dim, const
     // row of 4096 bf16 takes a block's threads once.
     // bf16, two against one: 131,072 tokens x 1280 124 us (306), 8192 x 4096 26.1 (32.5), 2048 x 4096 5.9 (7.2); 1024 x
     // 4096, below the rule, 4.8 (4.8). What bounds it then is HBM: 8192 x 4096 distinct rows move 134 MB, 5.1 TB/s.
+    // Rows that are not whole vectors go by two elements or one: 131,072 uniform tokens of 65,536 rows, 1282 columns
+    // 260 us and 1281 303, 1280 131 (each after a write of 256 MB). (148: the SMs this library is built for.)
     const int64_t vecs = dim / vec, each = kLookupLoads / 2;
     const bool two = n * std::min<int64_t>(vecs, kLookupThreads) >= (int64_t)2048 * 148;
     A.lanes = (int)std::min<int64_t>(kLookupThreads, two ? (vecs + each - 1) / each : vecs);

@@ -16,7 +16,7 @@
 //    copies its eight 16-byte words of a chunk into its own slots of shared
 //    memory (cp.async), two chunks ahead of the one it sums, with no barrier,
 //    since no thread reads another's slots: 128 to 192 KB are in flight per SM
-//    throughout. 6.72 TB/s on 13.5 GB of bf16 gradients (four blocks with plain
+//    throughout. 6.6 TB/s on 13.5 GB of bf16 gradients (four blocks with plain
 //    loads: 4.83; three blocks with one chunk less ahead: 4.09).
 //  * Scaling in place: one block per chunk with plain streaming loads and
 //    stores, 64 registers, from the last chunk to the first, so that it begins
@@ -78,7 +78,9 @@ constexpr int kSmallWarps = kSmallBlocks * kSmallThreads / 32;
 // chunk (512 KB: clipped in 5.2 us, by the streaming kernels in 7.4; at 1 MB 9.3
 // against 7.4); one with more tensors, whose other way is the 31 KB table in
 // three launches, up to four chunks a warp (600 tensors of 100 values: 8.9
-// against 10.6 us; of 800 values: 10.4 against 10.6).
+// against 10.6 us; of 800 values: 10.4 against 10.6). Beyond kMidTable the table
+// would need a third block of 31 KB, for less: 900 tensors of 100 values 11.0
+// against 12.1 us, of 800 12.7 against 12.4.
 constexpr int small_chunks(size_t tensors) {
     return tensors <= kSmallTable ? kSmallWarps : tensors <= kMidTable ? 4 * kSmallWarps : 0;
 }
