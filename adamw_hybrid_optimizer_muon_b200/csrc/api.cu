@@ -623,7 +623,7 @@ int check_disjoint(std::vector<std::pair<uintptr_t, uintptr_t>>& w) {
 }
 
 int check_muon_call(int batch, int64_t R, int64_t C, float* const* W, const void* const* G, int gdt,
-                    float* const* M, const ma_muon_hparams_t* hp, MuonGeom* g) {
+                    float* const* M, const ma_muon_hparams_t* hp, const void* clip, MuonGeom* g) {
     int st = check_muon_hp(hp);
     if (st) return st;
     if (batch < 0 || R < 0 || C < 0) return MA_ERR_SHAPE;
@@ -642,6 +642,7 @@ int check_muon_call(int batch, int64_t R, int64_t C, float* const* W, const void
         w.push_back({(uintptr_t)W[b], (uintptr_t)W[b] + bytes});
         w.push_back({(uintptr_t)M[b], (uintptr_t)M[b] + bytes});
     }
+    if (clip) w.push_back({(uintptr_t)clip, (uintptr_t)clip + sizeof(ClipHead)});
     return check_disjoint(w);
 }
 
@@ -1429,7 +1430,7 @@ int muon_step_batched_clipped(int batch, int64_t R, int64_t C, float* const* W, 
                               float* const* M, const ma_muon_hparams_t* hp, const void* clip, void* ws,
                               size_t ws_bytes, void* stream) {
     MuonGeom g;
-    int st = check_muon_call(batch, R, C, W, G, gdt, M, hp, &g);
+    int st = check_muon_call(batch, R, C, W, G, gdt, M, hp, clip, &g);
     if (st) return st;
     if (!aligned(clip, kAlign)) return MA_ERR_ALIGN;
     if (g.total == 0) return MA_OK;
@@ -1563,6 +1564,7 @@ int adamw_step_fused_clipped(int n, float* const* P, const void* const* G, int g
         const uintptr_t bytes = (uintptr_t)it.numel * 4;
         for (const float* q : {it.p, it.m, it.v}) w.push_back({(uintptr_t)q, (uintptr_t)q + bytes});
     }
+    if (clip) w.push_back({(uintptr_t)clip, (uintptr_t)clip + sizeof(ClipHead)});
     if ((st = check_disjoint(w))) return st;
     if ((st = device_ok_and_sms(nullptr))) return st;
     AdamwGroupConst c = adamw_const(*hp);
@@ -2171,7 +2173,7 @@ static void* noalloc_scratch_ptr() {
 extern "C" int muon_step_batched_noalloc(int batch, int64_t R, int64_t C, float* const* W, const void* const* G,
                                          int gdt, float* const* M, const ma_muon_hparams_t* hp, void* stream) {
     MuonGeom g;
-    int st = check_muon_call(batch, R, C, W, G, gdt, M, hp, &g);
+    int st = check_muon_call(batch, R, C, W, G, gdt, M, hp, nullptr, &g);
     if (st) return st;
     if (g.total == 0) return MA_OK;
     if (g.total > MA_STATIC_SCRATCH_BYTES) return MA_ERR_WORKSPACE;

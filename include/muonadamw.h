@@ -336,7 +336,8 @@ int ma_clip_finalize(float scale, float max_norm, void* clip, void* stream);
 /* adamw_step_fused and muon_step_batched on gradients taken times the coef of
  * a clip buffer (filled by an earlier call on the stream) as they are read: no
  * pass over the gradients of its own, and the gradients stay as they are.
- * clip NULL: unclipped, the same bits as the functions without it. */
+ * clip NULL: unclipped, the same bits as the functions without it. MA_ERR_ARG
+ * when clip lies in a buffer that the step writes. */
 int adamw_step_fused_clipped(int n, float* const* P, const void* const* G, int gdt, float* const* M,
                              float* const* V, const int64_t* numel, const ma_adamw_hparams_t* hp,
                              const void* clip, void* stream);
