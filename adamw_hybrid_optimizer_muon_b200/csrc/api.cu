@@ -622,6 +622,12 @@ int check_disjoint(std::vector<std::pair<uintptr_t, uintptr_t>>& w) {
     return MA_OK;
 }
 
+// Whether a clip buffer, of which `bytes` are used, shares memory with a workspace.
+bool clip_meets(const void* clip, size_t bytes, const void* ws, size_t ws_bytes) {
+    const uintptr_t c = (uintptr_t)clip, w = (uintptr_t)ws;
+    return clip && ws && c < w + ws_bytes && w < c + bytes;
+}
+
 int check_muon_call(int batch, int64_t R, int64_t C, float* const* W, const void* const* G, int gdt,
                     float* const* M, const ma_muon_hparams_t* hp, const void* clip, MuonGeom* g) {
     int st = check_muon_hp(hp);
@@ -858,6 +864,8 @@ int check_step(ma_plan* plan, const ma_group_t* groups, void* ws, size_t ws_byte
         if (g.total > seg_limit(plan)) return MA_ERR_ARG;
     }
     if (plan->ws_bytes > 0 && (!ws || !aligned(ws, kAlign) || ws_bytes < plan->ws_bytes)) return MA_ERR_WORKSPACE;
+    if (clip_meets(plan->clip.clip, plan->measure ? MA_CLIP_BYTES : sizeof(ClipHead), ws, plan->ws_bytes))
+        return MA_ERR_ARG;
     *sms = 0;
     if (!plan->adamw_idx.empty() || !plan->buckets.empty()) {
         if ((st = device_ok_and_sms(sms))) return st;
@@ -1435,6 +1443,7 @@ int muon_step_batched_clipped(int batch, int64_t R, int64_t C, float* const* W, 
     if (!aligned(clip, kAlign)) return MA_ERR_ALIGN;
     if (g.total == 0) return MA_OK;
     if (!ws || !aligned(ws, kAlign) || ws_bytes < g.total) return MA_ERR_WORKSPACE;
+    if (clip_meets(clip, sizeof(ClipHead), ws, g.total)) return MA_ERR_ARG;
     int sms = 0;
     if ((st = device_ok_and_sms(&sms))) return st;
     // a large batch runs as consecutive sub-batches of at most kSubBatchBytes of

@@ -337,7 +337,7 @@ int ma_clip_finalize(float scale, float max_norm, void* clip, void* stream);
  * a clip buffer (filled by an earlier call on the stream) as they are read: no
  * pass over the gradients of its own, and the gradients stay as they are.
  * clip NULL: unclipped, the same bits as the functions without it. MA_ERR_ARG
- * when clip lies in a buffer that the step writes. */
+ * when clip lies in a buffer that the step writes, the workspace included. */
 int adamw_step_fused_clipped(int n, float* const* P, const void* const* G, int gdt, float* const* M,
                              float* const* V, const int64_t* numel, const ma_adamw_hparams_t* hp,
                              const void* clip, void* stream);
@@ -449,7 +449,7 @@ int muonadamw_step(ma_plan_t* plan, const ma_group_t* groups, void* ws, size_t w
  * ranks); scale and max_norm are not used. clip NULL turns it off again. The scale and max_norm may change
  * from step to step, also of a captured graph; another clip buffer captures
  * again. A step from host memory then starts its updates after the last copy.
- * MA_ERR_ARG when clip overlaps a planned buffer. */
+ * MA_ERR_ARG when clip overlaps a planned buffer (the steps: their workspace). */
 int ma_plan_set_clip(ma_plan_t* plan, int measure, float scale, float max_norm, void* clip);
 
 /* One MuonAdamW step whose gradients start in host memory (for example
