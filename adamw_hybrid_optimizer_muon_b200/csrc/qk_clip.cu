@@ -832,6 +832,18 @@ int qk_max(int64_t seqs, int64_t len, int64_t total, int heads, int kv_heads, in
             if (st[i] % 8 != 0) return MA_ERR_ALIGN;
             if (st[i] >= (int64_t(1) << 38)) return MA_ERR_UNSUPPORTED;
         }
+        // bytes from the first element of an input to its last (in floating point: strides times extents may be large)
+        auto bytes = [&](int i) {
+            double n = dim;
+            for (int d = i; d < i + 3; ++d) n += (double)(ext[d] - 1) * (double)st[d];
+            return 2.0 * n;
+        };
+        auto meets = [&](const void* p, double n) {
+            const uintptr_t a = reinterpret_cast<uintptr_t>(p), o = reinterpret_cast<uintptr_t>(out);
+            return a < o + 4 * (uintptr_t)heads && (o < a || (double)(o - a) < n);
+        };
+        if (meets(q, bytes(0)) || meets(k, bytes(3)) || (offsets && meets(offsets, 4.0 * (double)(seqs + 1))))
+            return MA_ERR_ARG;
     }
     const int n = tile_keys(dim);
     const int chunks = (dim + kBK - 1) / kBK;

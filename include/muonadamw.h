@@ -396,7 +396,8 @@ int ma_embed_grad(int64_t n, const void* ids, int idt, int64_t rows, int64_t dim
  *     more than len apart are cut to fit and record MA_ERR_BOUNDS in the status word.
  *  out: device, `heads` floats. accumulate 0: set; 1: the maximum with what is
  *     there (several calls make one batch). -infinity: no visible pair. A NaN
- *     logit, or a NaN that is there, makes its head's maximum NaN.
+ *     logit, or a NaN that is there, makes its head's maximum NaN. MA_ERR_ARG
+ *     when out lies within q, k or offsets (from their first element to the last).
  * fp32 accumulation of the exact bf16 products; a maximum does not depend on
  * the order, so the same inputs give the same bits. */
 int ma_qk_max_logit(int64_t seqs, int64_t len, int64_t total, int heads, int kv_heads, int dim,
