@@ -470,9 +470,10 @@ def _on_current_gpu(what: str, *tensors) -> None:
     for t in tensors:
         if t is None:
             continue
-        if current is None and t.is_cuda:
+        on = t.get_device()
+        if current is None and on >= 0:
             current = _torch()._C._cuda_getDevice()
-        if not t.is_cuda or t.get_device() != current:
+        if on != current or on < 0:
             raise MAError(MA_ERR_ARG, f"{what}: tensor on {t.device}, not on the current CUDA device")
 
 
@@ -980,24 +981,27 @@ class GradClip:
         self._read = (self.grads, _marshal().pointers(self.grads), _marshal().numels(self.grads))
         self._unchanged = _marshal().unchanged
         self._get_device = _torch()._C._cuda_getDevice
+        self._get_stream = _torch()._C._cuda_getCurrentRawStream
 
-    def _ready(self, what: str):
-        """Before a call: the device is the buffer's, and the tables are those of the gradients as they are."""
+    def _ready(self, what: str, stream) -> int:
+        """Before a call: the device is the buffer's, and the tables are those of the gradients as they are. The
+        stream's handle."""
         if self._get_device() != self._device:
             _on_current_gpu(what, self.buffer)
         if not self._unchanged(*self._read):
             self._read_gradients()
+        return self._get_stream(self._device) if stream is None else _stream(stream)
 
     def norm(self, max_norm: float = math.inf, scale: float = 1.0, stream=None):
         """Fill ``buffer``; the norm (times scale) as a 0-d view of it, on the device. The next call overwrites it."""
-        self._ready("GradClip.norm")
-        _check(lib().ma_grad_norm(*self._args, scale, max_norm, self._ptr, _stream(stream)), "ma_grad_norm")
+        at = self._ready("GradClip.norm", stream)
+        _check(lib().ma_grad_norm(*self._args, scale, max_norm, self._ptr, at), "ma_grad_norm")
         return self._norm
 
     def clip(self, max_norm: float, scale: float = 1.0, stream=None):
         """Scale and clip the gradients in place; returns their norm before clipping, as :meth:`norm` does."""
-        self._ready("GradClip.clip")
-        _check(lib().ma_grad_clip(*self._args, scale, max_norm, self._ptr, _stream(stream)), "ma_grad_clip")
+        at = self._ready("GradClip.clip", stream)
+        _check(lib().ma_grad_clip(*self._args, scale, max_norm, self._ptr, at), "ma_grad_clip")
         return self._norm
 
 
