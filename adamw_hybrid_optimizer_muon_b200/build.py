@@ -22,10 +22,13 @@ import subprocess
 import sys
 import sysconfig
 
-from . import _marshal_path
-
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
+if not __package__:  # run as a script
+    sys.path.insert(0, ROOT)
+
+from adamw_hybrid_optimizer_muon_b200 import _marshal_path  # noqa: E402
+
 CSRC = os.path.join(HERE, "csrc")
 OBJ = os.path.join(HERE, "_build")
 LIB_DIR = os.path.join(HERE, "lib")
