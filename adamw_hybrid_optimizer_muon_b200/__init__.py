@@ -301,6 +301,13 @@ def _stream(stream) -> int:
     return int(stream.cuda_stream)
 
 
+def _stream_object(handle: int, index: int | None = None):
+    """The torch stream of a handle. (ExternalStream takes the default stream's, 0, for none given, and hands out a
+    stream of torch's pool.)"""
+    cuda = _torch().cuda
+    return cuda.ExternalStream(handle, device=index) if handle else cuda.default_stream(index)
+
+
 def _dtype_code(t) -> int:
     torch = _torch()
     dt = t.dtype
@@ -577,8 +584,7 @@ def _on_stream(stream):
     if stream is None:
         return _HERE
     torch = _torch()
-    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(_stream(stream))
-    return torch.cuda.stream(s)
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else _stream_object(_stream(stream)))
 
 
 def _new(like, shape, dtype, stream):
@@ -656,7 +662,7 @@ def _sum_stream(index: int) -> int:
     stream = _torch()._C._cuda_getCurrentRawStream(index)
     known = _SUM_STREAMS.get(index)
     if known is None or stream not in known:
-        _SUM_STREAMS[index] = {**(known or {}), stream: _torch().cuda.ExternalStream(stream, device=index)}
+        _SUM_STREAMS[index] = {**(known or {}), stream: _stream_object(stream, index)}
     return stream
 
 
@@ -1182,7 +1188,7 @@ class MuonAdamW:
         self._set_clip(max_norm, grad_scale)
         self._advance()
         self._plan.step_from_host(host_grads, self.groups, stream, copy_stream)
-        cs = copy_stream if isinstance(copy_stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(copy_stream))
+        cs = copy_stream if isinstance(copy_stream, torch.cuda.Stream) else _stream_object(int(copy_stream))
         self.host_copies_done = torch.cuda.Event()
         self.host_copies_done.record(cs)
 
